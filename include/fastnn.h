@@ -293,10 +293,165 @@ int fastnn_reciprocal_noalloc(const void *desc1, int H1, int W1, const void *des
 int fastnn_noalloc_device_status(fastnn_stream_t stream);
 
 /*
+ * The token store: soft matching of one image's tokens (descriptors, patch
+ * features) with those of the earlier images of its stream.
+ *
+ * fastnn_nn answers a query with the one database row of the largest dot
+ * product. The calls below keep the rows of many images in a paged store and
+ * answer a query with the softmax-weighted mean of the stored values under
+ * the same dot products:
+ *   out[t, h] = sum_p w_p value[p],  w_p = exp(scale <q[t, h], key[p]> - lse)
+ * over the positions p of the token's own sequence (stream) that it sees.
+ *
+ * fastnn_store describes the store and one ragged batch of new tokens. Page
+ * ids are physical; position p of sequence s lives in row p % page of page
+ * page_table[s][p / page]. Tokens cu[s] .. cu[s + 1] - 1 of the batch belong
+ * to sequence s. Query heads share key heads in equal groups: head h of q
+ * reads key head h / (heads_q / heads). All index arrays are device int32;
+ * they are read on the device only, so a captured graph follows their
+ * contents. dtype is FASTNN_BF16 or FASTNN_F16 for keys, values, means,
+ * queries and outputs alike. k_pages, v_pages and k_mean are contiguous and
+ * 16-byte aligned.
+ *
+ * What the index arrays may hold (checked on the device, never read out of
+ * range): a page id outside [0, n_pages) is a hole, whose positions do not
+ * exist; positions past table_width * page do not exist; of a sequence with
+ * more than max_new new tokens only the first max_new are taken; tokens at or
+ * past cu[n_seqs] are left as they are, in the outputs too.
+ */
+typedef struct {
+    void *k_pages;             /* [n_pages][heads][page][d] keys */
+    void *v_pages;             /* [n_pages][heads][page][dv] values */
+    void *k_mean;              /* [n_pages][heads][d] mean key of each page, or NULL */
+    const int32_t *page_table; /* [n_seqs][table_width] physical page ids */
+    const int32_t *lens;       /* [n_seqs] positions held (each call says when) */
+    const int32_t *cu;         /* [n_seqs + 1] first new token of each sequence */
+    int64_t n_pages;           /* >= 1 */
+    int n_seqs;                /* 1 .. 65534 */
+    int table_width;           /* >= 1; table_width * page < 2^31 - 256 */
+    int page;                  /* positions in a page: 16, 32, 64 or 128 */
+    int heads;                 /* key / value heads, 1 .. 1024 */
+    int d;                     /* key elements: a multiple of 8, 8 .. 128 */
+    int dv;                    /* value elements: a multiple of 8, 8 .. 128 */
+    int dtype;                 /* FASTNN_BF16 or FASTNN_F16 */
+} fastnn_store;
+
+/* How the pairs that turn together lie in the rotated elements of one axis:
+ * element j with j + half, or 2j with 2j + 1. */
+typedef enum {
+    FASTNN_ROTARY_HALF = 0,
+    FASTNN_ROTARY_INTERLEAVED = 1
+} fastnn_rotary_layout;
+
+/*
+ * A position rotation. The first `rot` elements of a row are cut into `axes`
+ * equal parts, one for each position axis (a pixel has two); pair j of part a
+ * turns by the angle pos[token][a] * freq[j] (radians, formed in fp64, so that
+ * far positions keep their angle) and is multiplied by `scale`; the elements
+ * after `rot` stay. Scaled positions (for axes longer than those seen in
+ * training) are a matter of the freq table, and `scale` is the amplitude that
+ * some of them carry.
+ */
+typedef struct {
+    const int32_t *pos;  /* [tokens][axes] */
+    const double *freq;  /* [rot / (2 * axes)] radians per position */
+    int axes;            /* 1 or 2 */
+    int rot;             /* a multiple of 2 * axes, at most d; 0 = no rotation */
+    int layout;          /* fastnn_rotary_layout */
+    float scale;         /* finite */
+} fastnn_rotation;
+
+/*
+ * fastnn_rotary -- rotate the rows of x [n][heads][d] into out (same shape).
+ *   inverse != 0 turns by the negative angles (times the same scale): the
+ *   transposed map, which carries a gradient of out back to x.
+ *   Tokens are x_stride (out_stride) elements apart, heads d elements.
+ *   out may be x itself (same pointer and stride), else they must not
+ *   overlap. Computed in fp32 and rounded once. 1 <= d <= 1024, any alignment
+ *   (16-byte aligned rows are read widest). n == 0 is a no-op.
+ */
+int fastnn_rotary(const void *x, int64_t x_stride, int64_t n, int heads, int d,
+                  int dtype, const fastnn_rotation *rotation, int inverse,
+                  void *out, int64_t out_stride, fastnn_stream_t stream);
+
+/*
+ * fastnn_store_append -- put new keys and values into the store.
+ *   store->lens are the positions held BEFORE the call: token i of sequence s
+ *   becomes position lens[s] + i. k [n][heads][d] (token stride k_stride) is
+ *   rotated on the way (rotation may be NULL), computed in fp32 and rounded
+ *   once; v [n][heads][dv] (v_stride) is copied.
+ *   If store->k_mean is given, the mean of every page that receives a token is
+ *   written anew: the mean over the keys the page then holds, as stored,
+ *   summed in fp32 and rounded once. Untouched pages keep theirs.
+ *   The caller advances lens. Pages that receive tokens must not be shared by
+ *   two sequences of the batch. k and v rows 16-byte aligned.
+ *   A new token that has no place (a hole, or a position past the table) is
+ *   not stored; fastnn_device_status() then reports FASTNN_ERR_INVALID, as it
+ *   does for a sequence with a negative length or more than max_new tokens.
+ *   workspace: FASTNN_STORE_APPEND_WORKSPACE bytes. n == 0 is a no-op.
+ */
+#define FASTNN_STORE_APPEND_WORKSPACE 256
+int fastnn_store_append(const fastnn_store *store, const void *k, int64_t k_stride,
+                        const void *v, int64_t v_stride, int64_t n, int max_new,
+                        const fastnn_rotation *rotation, void *workspace,
+                        size_t workspace_bytes, fastnn_stream_t stream);
+
+/*
+ * fastnn_attend -- attention of the batch's tokens over their sequences.
+ *   store->lens are the positions held INCLUDING the batch's tokens (append
+ *   first). Token i of the n_s new tokens of sequence s sees positions below
+ *   lens[s] (causal == 0) or below lens[s] - n_s + i + 1 (causal != 0).
+ *   q [n][heads_q][d], token stride q_stride, rows 16-byte aligned; heads_q a
+ *   multiple of store->heads. out [n][heads_q][dv] contiguous; lse (or NULL)
+ *   [n][heads_q] float32, the natural logarithm of the sum of the
+ *   exponentials. A token that sees nothing gets out = 0, lse = -infinity.
+ *   Products and sums in fp32; the weights of the second product are rounded
+ *   to dtype (relative 2^-9 for bf16, far below the rounding of a result that
+ *   averages them); out is rounded once.
+ *   Keys and values at positions that some token of the call sees must be
+ *   finite; what lies behind lens in a page is never used.
+ *   pages (or NULL): [n][heads][select] logical page numbers (position / page),
+ *   as fastnn_select_pages writes them: the token then sees only the positions
+ *   of the pages listed for its key head. Entries outside its sequence's pages
+ *   are skipped; a page that is listed twice counts twice.
+ *   workspace: fastnn_attend_workspace_size() with the same arguments (256-byte
+ *   aligned). n == 0 is a no-op.
+ */
+size_t fastnn_attend_workspace_size(const fastnn_store *store, int64_t n, int heads_q,
+                                    int max_new, int select);
+int fastnn_attend(const fastnn_store *store, const void *q, int64_t q_stride, int64_t n,
+                  int heads_q, int max_new, int causal, float scale, const int32_t *pages,
+                  int select, void *out, float *lse, void *workspace,
+                  size_t workspace_bytes, fastnn_stream_t stream);
+
+/*
+ * fastnn_select_pages -- the pages worth a query's attention, by a cheap score.
+ *   For each token t and key head g: the score of a page is the sum over the
+ *   query heads of the group of <q[t, h], k_mean[page]>; the token's first
+ *   keep_first and last keep_last visible pages are taken whatever their
+ *   score, the best others fill up to `select`. out_pages [n][heads][select]
+ *   int32: their logical numbers in ascending order, -1 behind the last.
+ *   Visible lengths are those of fastnn_attend (lens including the batch);
+ *   holes are never taken. The order of the scores is that of their fp64
+ *   values; among equal ones the lowest page is first; a NaN score is last.
+ *   Under causal, keep_last >= 1 keeps the mean of the page that holds the
+ *   token's own future out of the choice, so 1 <= keep_last; keep_first +
+ *   keep_last <= select <= 256. store->v_pages and k_pages are not read (may
+ *   be NULL); dv is not used but must be valid.
+ *   workspace: fastnn_select_workspace_size() bytes, 256-byte aligned.
+ */
+size_t fastnn_select_workspace_size(const fastnn_store *store, int64_t n);
+int fastnn_select_pages(const fastnn_store *store, const void *q, int64_t q_stride,
+                        int64_t n, int heads_q, int max_new, int causal, int keep_first,
+                        int keep_last, int select, int32_t *out_pages, void *workspace,
+                        size_t workspace_bytes, fastnn_stream_t stream);
+
+/*
  * fastnn_device_status -- synchronise `stream` and read the device status
  * word of the last call that used `workspace`: FASTNN_OK, or
  * FASTNN_ERR_TIMEOUT when a kernel's bounded wait ran out (its outputs are
- * then invalid). Blocks the host.
+ * then invalid), FASTNN_ERR_INVALID when fastnn_store_append met index arrays
+ * that leave a new token without a place. Blocks the host.
  */
 int fastnn_device_status(const void *workspace, fastnn_stream_t stream);
 

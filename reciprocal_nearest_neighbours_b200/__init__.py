@@ -47,3 +47,14 @@ from ._lib import (  # noqa: F401
     library_path,
     seed_count,
 )
+from ._store import (  # noqa: F401
+    FASTNN_ROTARY_HALF,
+    FASTNN_ROTARY_INTERLEAVED,
+    FASTNN_STORE_APPEND_WORKSPACE,
+    fastnn_attend,
+    fastnn_attend_workspace_size,
+    fastnn_rotary,
+    fastnn_rotary_frequencies,
+    fastnn_select_pages,
+    fastnn_store_append,
+)

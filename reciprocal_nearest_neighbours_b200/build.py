@@ -12,8 +12,10 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfastnn.so")
-SOURCES = ["api.cu", "nn_tc.cu", "l2_nn.cu", "frontier.cu", "noalloc.cu"]
-HEADERS = ["common.cuh", "ptx.cuh", "nn_tc.cuh", "l2_nn.cuh", "frontier.cuh", "frontier_dev.cuh"]
+SOURCES = ["api.cu", "nn_tc.cu", "l2_nn.cu", "frontier.cu", "noalloc.cu", "rotary.cu", "attend.cu",
+           "select.cu", "store_api.cu"]
+HEADERS = ["common.cuh", "ptx.cuh", "nn_tc.cuh", "l2_nn.cuh", "frontier.cuh", "frontier_dev.cuh",
+           "store.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 
@@ -36,7 +38,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     cmd = [nvcc(), "-O3", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
+           "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-t", "0",
            "-I", INCLUDE, "-o", LIB + ".tmp"]
     if verbose:
         cmd += ["-Xptxas", "-v"]

@@ -8,6 +8,7 @@
 #include "frontier.cuh"
 #include "l2_nn.cuh"
 #include "nn_tc.cuh"
+#include "store.cuh"
 
 using namespace fastnn;
 
@@ -179,6 +180,10 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
   } while (0)
 
 }  // namespace
+
+namespace fastnn {
+uint64_t wait_timeout_ns() { return g_wait_ns.load(); }
+}  // namespace fastnn
 
 extern "C" {
 
@@ -594,7 +599,8 @@ int fastnn_device_status(const void* workspace, fastnn_stream_t stream) {
   int h = 0;
   FASTNN_CUDA_TRY(cudaMemcpyAsync(&h, workspace, sizeof(int), cudaMemcpyDeviceToHost, st));
   FASTNN_CUDA_TRY(cudaStreamSynchronize(st));
-  return (h & kStatusTimeout) ? FASTNN_ERR_TIMEOUT : FASTNN_OK;
+  if (h & kStatusTimeout) return FASTNN_ERR_TIMEOUT;
+  return (h & kStatusStoreIndex) ? FASTNN_ERR_INVALID : FASTNN_OK;
 }
 
 int fastnn_kernel_timer_enable(int capacity) { return kernel_timer_enable(capacity); }

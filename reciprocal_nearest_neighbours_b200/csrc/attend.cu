@@ -1,0 +1,505 @@
+// Attention over the paged token store, few query rows at a time.
+//
+//     out[t, h] = sum_p exp2(x_p - lse2) value[p],  x_p = scale * log2(e) * <q[t, h], key[p]>
+//
+// in one pass over the keys: a running maximum m, sum l and output O per row,
+//     m' = max(m, max x),  l' = l 2^(m - m') + sum 2^(x - m'),
+//     O' = O 2^(m - m') + 2^(x - m') V,
+// all in fp32. A block takes 16 rows of one sequence and key head (the rows are
+// (token, query head of the group), so a group's heads share the keys' read) and
+// one split of the positions. Its warps do not wait for one another: each
+// streams every kWarps-th unit of 16 positions through its own cp.async ring,
+// keeps its own (m, l, O), and the warps merge once at the end. Splits leave
+// normalised partial outputs with their log2 sums, which combine_kernel weighs.
+// With few rows the work is bound by reading K and V once; the 16-row mma.sync
+// tile (m16n8k16) fits the few rows, and its rate is far from binding.
+#include <type_traits>
+
+#include "store.cuh"
+#include "ptx.cuh"
+
+namespace fastnn {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRows = 16;    // query rows of a block (one mma tile)
+constexpr int kUnit = 16;    // positions of a unit: the smallest page
+constexpr int kStages = 3;   // units in a warp's ring
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
+  const int bytes = real ? 16 : 0;  // 0: the 16 bytes are zero-filled, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile of DP 16-bit elements a
+// row. Chunks are permuted so that eight consecutive rows of one chunk column
+// (an ldmatrix access) fall into eight different bank groups.
+template <int DP>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  if constexpr (DP >= 64) return static_cast<uint32_t>(r * DP * 2 + ((c ^ (r & 7)) << 4));
+  return static_cast<uint32_t>(r * DP * 2 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+template <int DP>
+struct RowsSmem {
+  static constexpr int kTile = kUnit * DP * 2;       // bytes of one K or V unit
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kRing = kStages * kStage;     // a warp's ring
+  static constexpr int kMl = kWarps * kRing;         // then [kWarps][16] m and l
+  static constexpr int kTotal = kMl + kWarps * kRows * 2 * 4;
+  static_assert(kRing >= kRows * DP * 4, "the merge reuses the ring");
+};
+
+// DP: head width padded to 32, 64 or 128. SEL: the positions are those of
+// a.pages' entries for the block's (single) token.
+template <typename T, int DP, bool SEL>
+__global__ void __launch_bounds__(kThreads)
+attend_rows_kernel(AttendArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  using S = RowsSmem<DP>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int s = blockIdx.z, g = blockIdx.y;
+  const int split = static_cast<int>(blockIdx.x) % a.splits;
+  const int tile = static_cast<int>(blockIdx.x) / a.splits;
+  if (blockIdx.x == 0 && g == 0 && s == 0 && tid == 0) *a.status = 0;
+  const StoreArgs& st = a.st;
+  const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
+
+  // The block's rows: row r is token tok(r) of the sequence, query head
+  // head(r); nrows of the 16 exist.
+  int r0, nrows, tok_first;
+  if constexpr (SEL) {
+    const int per_tok = (a.group + kRows - 1) / kRows;
+    tok_first = tile / per_tok;
+    if (tok_first >= w.n) return;
+    r0 = (tile - tok_first * per_tok) * kRows;
+    nrows = a.group - r0 < kRows ? a.group - r0 : kRows;
+  } else {
+    r0 = tile * kRows;
+    const int64_t all = static_cast<int64_t>(w.n) * a.group;
+    if (r0 >= all) return;
+    nrows = all - r0 < kRows ? static_cast<int>(all - r0) : kRows;
+    tok_first = r0 / a.group;
+  }
+  const int last = SEL ? tok_first : (r0 + nrows - 1) / a.group;
+  const int vmax = visible(w, last);  // visible() grows with the token
+
+  int u_count;      // units of the whole block
+  int k0 = 0;       // first position (not SEL)
+  const int32_t* list = nullptr;
+  const int upp = st.page / kUnit;
+  if constexpr (SEL) {
+    const int e0 = split * a.split_len;
+    const int e1 = e0 + a.split_len < a.select ? e0 + a.split_len : a.select;
+    list = a.pages + ((static_cast<int64_t>(w.t0) + tok_first) * st.heads + g) * a.select + e0;
+    u_count = e1 > e0 ? (e1 - e0) * upp : 0;
+  } else {
+    k0 = split * a.split_len;
+    if (split > 0 && k0 >= vmax) return;  // no row of the tile reads this split
+    const int k1 = vmax - k0 < a.split_len ? vmax : k0 + a.split_len;
+    u_count = (k1 - k0 + kUnit - 1) / kUnit;
+  }
+
+  // Query fragments (rows lane / 4 and + 8), zero beyond d and beyond nrows.
+  uint32_t qa[DP / 16][4];
+  int vis[2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = (lane >> 2) + 8 * half;
+    const bool real = r < nrows;
+    const int rr = r0 + (real ? r : 0);
+    const int tok = SEL ? tok_first : rr / a.group;
+    const int hd = g * a.group + (SEL ? rr : rr - tok * a.group);
+    vis[half] = real ? visible(w, tok) : 0;
+    const uint16_t* qr = a.q + (static_cast<int64_t>(w.t0) + tok) * a.q_stride +
+                         static_cast<int64_t>(hd) * st.d;
+#pragma unroll
+    for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = ks * 16 + c * 8 + (lane & 3) * 2;
+        qa[ks][half + 2 * c] =
+            real && col < st.d ? __ldg(reinterpret_cast<const uint32_t*>(qr + col)) : 0u;
+      }
+  }
+  const int vmin_lane = vis[0] < vis[1] ? vis[0] : vis[1];
+  const int vmin = __reduce_min_sync(0xffffffffu, vmin_lane);
+
+  const uint32_t ring = ptx::smem_u32(smem) + warp * S::kRing;
+  const int mine = u_count > warp ? (u_count - warp + kWarps - 1) / kWarps : 0;
+
+  // Page ids of 32 of this warp's units at a time, one a lane: the physical
+  // page (-1: hole) and, for SEL, the logical page.
+  int ids = -1, lps = 0;
+  auto fetch_ids = [&](int j) {
+    const int u = warp + (j + lane) * kWarps;
+    ids = -1;
+    if (u < u_count) {
+      int lp;
+      if constexpr (SEL) {
+        lp = __ldg(list + u / upp);
+      } else {
+        lp = (k0 + u * kUnit) >> st.page_log2;
+      }
+      lps = lp;
+      if (lp >= 0 && lp < st.width) {
+        const int id = __ldg(st.table + static_cast<int64_t>(s) * st.width + lp);
+        if (id >= 0 && id < st.n_pages) ids = id;
+      }
+    }
+  };
+  // First position of unit j of this warp; its id decides whether it exists.
+  auto unit_pos = [&](int j, int lp) {
+    const int u = warp + j * kWarps;
+    if constexpr (SEL) return lp * st.page + (u % upp) * kUnit;
+    return k0 + u * kUnit;
+  };
+  // Positions of the ring's stages (-1: nothing there), as the warp knows them.
+  int pos_ring[kStages];
+  auto issue = [&](int j) {
+    int pos = -1;
+    if (j < mine) {
+      if ((j & 31) == 0) fetch_ids(j);
+      const int id = __shfl_sync(0xffffffffu, ids, j & 31);
+      const int lp = SEL ? __shfl_sync(0xffffffffu, lps, j & 31) : 0;
+      if (id >= 0) pos = unit_pos(j, lp);
+      if (pos >= vmax) pos = -1;
+      if (pos >= 0) {
+        const int64_t row =
+            (static_cast<int64_t>(id) * st.heads + g) * st.page + (pos & (st.page - 1));
+        const uint16_t* kp = st.k + row * st.d;
+        const uint16_t* vp = st.v + row * st.dv;
+        const uint32_t kd = ring + (j % kStages) * S::kStage, vd = kd + S::kTile;
+        constexpr int kChunks = DP / 8;
+#pragma unroll
+        for (int i = 0; i < kUnit * kChunks / 32; ++i) {
+          const int c = (i * 32 + lane) % kChunks, r = (i * 32 + lane) / kChunks;
+          const bool there = pos + r < vmax;  // what lies behind the length is not read
+          const bool kr = there && c * 8 < st.d, vr = there && c * 8 < st.dv;
+          cp16(kd + chunk_at<DP>(r, c), kr ? kp + r * st.d + c * 8 : st.k, kr);
+          cp16(vd + chunk_at<DP>(r, c), vr ? vp + r * st.dv + c * 8 : st.v, vr);
+        }
+      }
+    }
+    cp_commit();
+    return pos;
+  };
+
+  float o[DP / 8][4] = {};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < kStages - 1; ++j) pos_ring[j] = issue(j);
+  for (int jb = 0; jb < mine; jb += kStages) {
+#pragma unroll
+    for (int st_i = 0; st_i < kStages; ++st_i) {
+      const int j = jb + st_i;
+      if (j >= mine) break;
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      const int pos = pos_ring[st_i];
+      // The stage read at step j - 1 is free again: fill it before computing.
+      pos_ring[(st_i + kStages - 1) % kStages] = issue(j + kStages - 1);
+      if (pos < 0) continue;
+      const uint32_t kd = ring + st_i * S::kStage, vd = kd + S::kTile;
+      float x[2][4] = {};
+      {
+        const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) {
+          uint32_t b[4];
+          ldsm4(kd + chunk_at<DP>(kr, ks * 2 + kc), b);
+          mma16816<T>(x[0], qa[ks], b[0], b[1]);
+          mma16816<T>(x[1], qa[ks], b[2], b[3]);
+        }
+      }
+      const bool edge = pos + kUnit > vmin;
+      float top[2] = {m[0], m[1]};
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[t][e] *= a.scale_log2;
+          if (edge && pos + t * 8 + (lane & 3) * 2 + (e & 1) >= vis[e >> 1]) x[t][e] = -INFINITY;
+          top[e >> 1] = fmaxf(top[e >> 1], x[t][e]);
+        }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 1));
+        top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 2));
+      }
+      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+        // A row that has seen nothing yet has m = -inf: l and O are 0 then.
+        const float f0 = m[0] == top[0] ? 1.f : ex2(m[0] - top[0]);
+        const float f1 = m[1] == top[1] ? 1.f : ex2(m[1] - top[1]);
+        l[0] *= f0;
+        l[1] *= f1;
+        m[0] = top[0];
+        m[1] = top[1];
+#pragma unroll
+        for (int t = 0; t < DP / 8; ++t) {
+          o[t][0] *= f0;
+          o[t][1] *= f0;
+          o[t][2] *= f1;
+          o[t][3] *= f1;
+        }
+      }
+      const float z0 = m[0] == -INFINITY ? 0.f : m[0], z1 = m[1] == -INFINITY ? 0.f : m[1];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        x[t][0] = ex2(x[t][0] - z0);
+        x[t][1] = ex2(x[t][1] - z0);
+        x[t][2] = ex2(x[t][2] - z1);
+        x[t][3] = ex2(x[t][3] - z1);
+        l[0] += x[t][0] + x[t][1];
+        l[1] += x[t][2] + x[t][3];
+      }
+      // The weights go to the tensor cores in the store's 16-bit type.
+      const uint32_t p[4] = {Half16<T>::pack(x[0][0], x[0][1]), Half16<T>::pack(x[0][2], x[0][3]),
+                             Half16<T>::pack(x[1][0], x[1][1]), Half16<T>::pack(x[1][2], x[1][3])};
+      const int vr = lane & 15, vc = lane >> 4;
+#pragma unroll
+      for (int t = 0; t < DP / 16; ++t) {
+        uint32_t b[4];
+        ldsm4t(vd + chunk_at<DP>(vr, t * 2 + vc), b);
+        mma16816<T>(o[2 * t], p, b[0], b[1]);
+        mma16816<T>(o[2 * t + 1], p, b[2], b[3]);
+      }
+    }
+  }
+  cp_wait<0>();
+  __syncwarp();
+
+  // Merge the warps: each leaves its rows' O (over its own ring), m and l.
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+    l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+  }
+  float* mine_o = reinterpret_cast<float*>(smem + warp * S::kRing);
+  float* ml = reinterpret_cast<float*>(smem + S::kMl);
+  {
+    const int r = lane >> 2, c = (lane & 3) * 2;
+#pragma unroll
+    for (int t = 0; t < DP / 8; ++t) {
+      *reinterpret_cast<float2*>(mine_o + r * DP + t * 8 + c) = make_float2(o[t][0], o[t][1]);
+      *reinterpret_cast<float2*>(mine_o + (r + 8) * DP + t * 8 + c) = make_float2(o[t][2], o[t][3]);
+    }
+    if ((lane & 3) == 0) {
+      ml[(warp * kRows + r) * 2] = m[0];
+      ml[(warp * kRows + r) * 2 + 1] = l[0];
+      ml[(warp * kRows + r + 8) * 2] = m[1];
+      ml[(warp * kRows + r + 8) * 2 + 1] = l[1];
+    }
+  }
+  __syncthreads();
+  const int r = tid >> 3;  // 8 threads a row
+  if (r >= nrows) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < kWarps; ++q) top = fmaxf(top, ml[(q * kRows + r) * 2]);
+  float f[kWarps], sum = 0.f;
+#pragma unroll
+  for (int q = 0; q < kWarps; ++q) {
+    const float mq = ml[(q * kRows + r) * 2];
+    f[q] = mq == -INFINITY ? 0.f : mq == top ? 1.f : ex2(mq - top);
+    sum += f[q] * ml[(q * kRows + r) * 2 + 1];
+  }
+  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+  const float lse2 = sum > 0.f ? top + log2f(sum) : sum == 0.f ? -INFINITY : sum;
+  const int rr = r0 + r;
+  const int tok = SEL ? tok_first : rr / a.group;
+  const int hd = g * a.group + (SEL ? rr : rr - tok * a.group);
+  const int64_t row = (static_cast<int64_t>(w.t0) + tok) * a.hq + hd;
+  const bool whole = SEL ? a.splits == 1 : visible(w, tok) <= a.split_len;
+  if (whole && split > 0) return;
+  for (int c = (tid & 7) * 4; c < st.dv; c += 32) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) {
+      const float4 y = *reinterpret_cast<const float4*>(
+          reinterpret_cast<const float*>(smem + q * S::kRing) + r * DP + c);
+      v.x += f[q] * y.x;
+      v.y += f[q] * y.y;
+      v.z += f[q] * y.z;
+      v.w += f[q] * y.w;
+    }
+    v.x *= inv;
+    v.y *= inv;
+    v.z *= inv;
+    v.w *= inv;
+    if (whole) {
+      *reinterpret_cast<uint2*>(a.out + row * st.dv + c) =
+          make_uint2(Half16<T>::pack(v.x, v.y), Half16<T>::pack(v.z, v.w));
+    } else {
+      *reinterpret_cast<float4*>(a.part + (split * a.n * a.hq + row) * st.dv + c) = v;
+    }
+  }
+  if ((tid & 7) == 0) {
+    if (!whole) {
+      a.part_lse[split * a.n * a.hq + row] = lse2;
+    } else if (a.lse) {
+      a.lse[row] = lse2 * 0.69314718055994530942f;  // ln 2
+    }
+  }
+}
+
+// Joins the splits of each row: out = sum_i 2^(lse2_i - lse2) out_i. A warp
+// takes one row.
+template <typename T, bool SEL>
+__global__ void __launch_bounds__(128)
+combine_kernel(AttendArgs a) {
+  const StoreArgs& st = a.st;
+  const int s = blockIdx.y, lane = threadIdx.x & 31;
+  const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (r >= static_cast<int64_t>(w.n) * a.hq) return;
+  const int tok = static_cast<int>(r / a.hq);
+  const int vis = visible(w, tok);
+  const int parts = SEL ? a.splits : (vis + a.split_len - 1) / a.split_len;
+  if (parts <= 1) return;  // its one split has written the result
+  const int64_t row = static_cast<int64_t>(w.t0) * a.hq + r;
+  const int64_t step = a.n * a.hq;
+  float top = -INFINITY;
+  for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_lse[i * step + row]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int c = lane * 4;
+  if (top > -INFINITY) {
+    for (int i = 0; i < parts; ++i) {
+      const float f = ex2(a.part_lse[i * step + row] - top);
+      sum += f;
+      if (c < st.dv) {
+        const float4 y = *reinterpret_cast<const float4*>(a.part + (i * step + row) * st.dv + c);
+        v.x += f * y.x;
+        v.y += f * y.y;
+        v.z += f * y.z;
+        v.w += f * y.w;
+      }
+    }
+    const float inv = 1.f / sum;
+    v.x *= inv;
+    v.y *= inv;
+    v.z *= inv;
+    v.w *= inv;
+  }
+  if (c < st.dv)
+    *reinterpret_cast<uint2*>(a.out + row * st.dv + c) =
+        make_uint2(Half16<T>::pack(v.x, v.y), Half16<T>::pack(v.z, v.w));
+  if (lane == 0 && a.lse)
+    a.lse[row] = top > -INFINITY ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+}
+
+template <typename T, int DP, bool SEL>
+int rows_launch(const AttendArgs& a, cudaStream_t st) {
+  using S = RowsSmem<DP>;
+  static_assert(S::kTotal <= 227 * 1024, "shared memory of an SM");
+  FASTNN_CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<T, DP, SEL>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal));
+  const int64_t tiles =
+      SEL ? static_cast<int64_t>(a.max_new) * ((a.group + kRows - 1) / kRows)
+          : (static_cast<int64_t>(a.max_new) * a.group + kRows - 1) / kRows;
+  if (tiles * a.splits > INT32_MAX) return FASTNN_ERR_INVALID;
+  const dim3 grid(static_cast<unsigned>(tiles * a.splits), a.st.heads, a.st.n_seqs);
+  attend_rows_kernel<T, DP, SEL><<<grid, kThreads, S::kTotal, st>>>(a);
+  FASTNN_CUDA_TRY(cudaGetLastError());
+  if (a.splits > 1) {
+    const int64_t blocks = (static_cast<int64_t>(a.max_new) * a.hq + 3) / 4;
+    combine_kernel<T, SEL><<<dim3(static_cast<unsigned>(blocks), a.st.n_seqs), 128, 0, st>>>(a);
+    FASTNN_CUDA_TRY(cudaGetLastError());
+  }
+  return FASTNN_OK;
+}
+
+template <typename T, bool SEL>
+int rows_width(const AttendArgs& a, cudaStream_t st) {
+  const int wide = a.st.d > a.st.dv ? a.st.d : a.st.dv;
+  if (wide <= 32) return rows_launch<T, 32, SEL>(a, st);
+  if (wide <= 64) return rows_launch<T, 64, SEL>(a, st);
+  return rows_launch<T, 128, SEL>(a, st);
+}
+
+}  // namespace
+
+// How many blocks share the positions of a row tile. The lengths are on the
+// device; the table's width bounds them. About four waves of blocks (two a SM)
+// even out ragged lengths, a split is at least 256 positions (four pages of a
+// selection) long, and splits beyond a row's length cost an empty block each.
+void attend_plan(AttendArgs& a) {
+  const bool sel = a.pages != nullptr;
+  const int64_t rows = static_cast<int64_t>(a.max_new) * a.group;
+  const int64_t tiles = sel ? static_cast<int64_t>(a.max_new) * ((a.group + kRows - 1) / kRows)
+                            : (rows + kRows - 1) / kRows;
+  const int64_t base = tiles * a.st.heads * a.st.n_seqs;
+  const int64_t want = 4 * 2 * 148;
+  int64_t splits = base >= want ? 1 : (want + base - 1) / base;
+  if (sel) {
+    const int64_t most = (a.select + 3) / 4;
+    if (base >= 148) splits = 1;  // entries are of one length: a wave is enough
+    if (splits > most) splits = most;
+    a.split_len = static_cast<int>((a.select + splits - 1) / splits);
+    a.splits = (a.select + a.split_len - 1) / a.split_len;
+    return;
+  }
+  const int64_t cap = static_cast<int64_t>(a.st.width) * a.st.page;
+  int64_t len = (cap + splits - 1) / splits;
+  if (len < 256) len = 256;
+  len = (len + 127) / 128 * 128;
+  if (len > (int64_t{1} << 30)) len = int64_t{1} << 30;
+  a.split_len = static_cast<int>(len);
+  a.splits = static_cast<int>((cap + len - 1) / len);
+}
+
+int launch_attend_rows(const AttendArgs& a, int dtype, cudaStream_t st) {
+  if (dtype == FASTNN_BF16)
+    return a.pages ? rows_width<__nv_bfloat16, true>(a, st) : rows_width<__nv_bfloat16, false>(a, st);
+  return a.pages ? rows_width<__half, true>(a, st) : rows_width<__half, false>(a, st);
+}
+
+}  // namespace fastnn

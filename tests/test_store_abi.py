@@ -1,0 +1,164 @@
+"""Host-side checks of the token store calls (no GPU): refusals and workspace sizes."""
+
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+import reciprocal_nearest_neighbours_b200 as fnn
+from reciprocal_nearest_neighbours_b200 import _store, build as fnn_build
+
+P = ctypes.c_void_p
+FAKE = 1 << 20  # an aligned address that no refused call reads
+
+
+@pytest.fixture(scope="module")
+def lib():
+    fnn_build.build()
+    return _store._lib()
+
+
+def _desc(**kw):
+    f = dict(k_pages=FAKE, v_pages=FAKE, k_mean=FAKE, page_table=FAKE, lens=FAKE, cu=FAKE, n_pages=9,
+             n_seqs=2, table_width=4, page=16, heads=2, d=64, dv=64, dtype=fnn.FASTNN_BF16)
+    f.update(kw)
+    return _store._Store(**f)
+
+
+def _rot(**kw):
+    f = dict(pos=FAKE, freq=FAKE, axes=1, rot=64, layout=0, scale=1.0)
+    f.update(kw)
+    return _store._Rotation(**f)
+
+
+STORE_FAULTS = [
+    (dict(dtype=fnn.FASTNN_I8), -2), (dict(dtype=fnn.FASTNN_F32_L2), -2), (dict(dtype=9), -2),
+    (dict(d=0), -2), (dict(d=12), -2), (dict(d=136), -2), (dict(dv=4), -2), (dict(dv=256), -2),
+    (dict(page=8), -2), (dict(page=48), -2), (dict(page=256), -2), (dict(page=0), -2),
+    (dict(n_seqs=0), -1), (dict(n_seqs=65535), -1), (dict(heads=0), -1), (dict(heads=1025), -1),
+    (dict(n_pages=0), -1), (dict(n_pages=1 << 31), -1), (dict(table_width=0), -1),
+    (dict(table_width=1 << 27), -1),
+]
+
+
+@pytest.mark.parametrize("change,status", STORE_FAULTS)
+def test_store_sizes_are_refused(lib, change, status):
+    s = _desc(**change)
+    big = 1 << 40
+    assert lib.fastnn_store_append(s, FAKE, 8192, FAKE, 8192, 5, 3, None, FAKE, 256, None) == status
+    assert lib.fastnn_attend(s, FAKE, 8192, 5, 2 * max(1, s.heads), 3, 1, 1.0, None, 0, FAKE, FAKE, FAKE,
+                             big, None) == status
+    assert lib.fastnn_select_pages(s, FAKE, 8192, 5, 2 * max(1, s.heads), 3, 1, 0, 1, 4, FAKE, FAKE, big,
+                                   None) == status
+    assert lib.fastnn_attend_workspace_size(s, 5, 2 * max(1, s.heads), 3, 0) == 0
+    assert lib.fastnn_select_workspace_size(s, 5) == 0
+
+
+def test_append_refusals(lib):
+    def call(s=None, k=FAKE, ks=128, v=FAKE, vs=128, n=5, m=3, r=None, ws=FAKE, nb=256):
+        return lib.fastnn_store_append(s or _desc(), k, ks, v, vs, n, m, r, ws, nb, None)
+    assert lib.fastnn_store_append(None, FAKE, 128, FAKE, 128, 5, 3, None, FAKE, 256, None) == -1
+    assert call(n=0, k=None, v=None, ws=None) == 0  # nothing to do
+    assert call(n=-1) == -1 and call(n=1 << 31) == -1 and call(m=0) == -1 and call(m=6) == -1
+    assert call(k=None) == -1 and call(v=None) == -1 and call(k=FAKE + 8) == -1 and call(v=FAKE + 2) == -1
+    assert call(ks=120) == -1 and call(ks=132) == -1 and call(vs=64) == -1
+    assert call(ws=None) == -1 and call(ws=FAKE + 16) == -1 and call(nb=255) == -3
+    for name in ("k_pages", "v_pages", "page_table", "lens", "cu"):
+        assert call(_desc(**{name: None})) == -1, name
+    assert call(_desc(k_pages=FAKE + 8)) == -1 and call(_desc(k_mean=FAKE + 8)) == -1
+    for change, status in ((dict(axes=0), -1), (dict(axes=3), -1), (dict(rot=65), -1), (dict(rot=66), -1),
+                           (dict(rot=-2), -1), (dict(axes=2, rot=6), -1), (dict(layout=2), -2),
+                           (dict(pos=None), -1), (dict(freq=None), -1), (dict(scale=float("nan")), -1),
+                           (dict(scale=float("inf")), -1)):
+        assert call(r=_rot(**change)) == status, change
+
+
+def test_rotary_refusals(lib):
+    def call(x=FAKE, xs=128, n=5, heads=2, d=64, dt=fnn.FASTNN_F16, r=None, out=FAKE, os=128):
+        return lib.fastnn_rotary(x, xs, n, heads, d, dt, r or _rot(), 0, out, os, None)
+    assert call(n=0, x=None, out=None) == 0
+    assert call(dt=fnn.FASTNN_I8) == -2 and call(d=0) == -2 and call(d=1025) == -2
+    assert call(n=-1) == -1 and call(heads=0) == -1 and call(xs=127) == -1 and call(os=100) == -1
+    assert call(x=None) == -1 and call(out=None) == -1 and call(x=FAKE + 1) == -1
+    assert call(os=136) == -1  # in place with another stride
+    assert call(r=_rot(rot=0)) == -1 and call(r=_rot(rot=66)) == -1 and call(r=_rot(layout=7)) == -2
+    assert lib.fastnn_rotary(FAKE, 128, 5, 2, 64, fnn.FASTNN_F16, None, 0, FAKE, 128, None) == -1
+
+
+def test_attend_refusals(lib):
+    big = 1 << 40
+
+    def call(s=None, q=FAKE, qs=256, n=5, hq=4, m=3, scale=1.0, pages=None, sel=0, out=FAKE, ws=FAKE,
+             nb=big, lse=FAKE):
+        return lib.fastnn_attend(s or _desc(), q, qs, n, hq, m, 1, scale, pages, sel, out, lse, ws, nb, None)
+    assert call(n=0, q=None, out=None, ws=None) == 0
+    assert call(hq=3) == -1 and call(hq=0) == -1 and call(m=0) == -1 and call(m=6) == -1 and call(n=-2) == -1
+    assert call(q=None) == -1 and call(q=FAKE + 4) == -1 and call(qs=200) == -1 and call(qs=260) == -1
+    assert call(out=None) == -1 and call(out=FAKE + 8) == -1 and call(lse=FAKE + 2) == -1
+    assert call(ws=None) == -1 and call(ws=FAKE + 128) == -1 and call(nb=64) == -3
+    assert call(scale=float("nan")) == -1 and call(scale=float("inf")) == -1
+    assert call(pages=FAKE) == -1 and call(sel=4) == -1 and call(pages=FAKE, sel=-1) == -1
+    for name in ("k_pages", "v_pages", "page_table", "lens", "cu"):
+        assert call(_desc(**{name: None})) == -1, name
+
+
+def test_select_refusals(lib):
+    def call(s=None, q=FAKE, qs=256, n=5, hq=4, m=3, first=0, last=1, sel=4, out=FAKE, ws=FAKE, nb=1 << 40):
+        return lib.fastnn_select_pages(s or _desc(), q, qs, n, hq, m, 1, first, last, sel, out, ws, nb, None)
+    assert call(n=0, q=None, out=None, ws=None) == 0
+    assert call(sel=0) == -1 and call(sel=257) == -1 and call(last=0) == -1 and call(first=-1) == -1
+    assert call(first=4) == -1 and call(first=2, last=3) == -1 and call(hq=5) == -1
+    assert call(out=None) == -1 and call(q=None) == -1 and call(ws=None) == -1 and call(nb=0) == -3
+    assert call(_desc(k_mean=None)) == -1
+    assert call(_desc(table_width=1 << 20)) == -2  # more pages than a block's shared memory scores
+
+
+def test_workspace_sizes(lib):
+    size = lambda n, m, sel=0, **kw: lib.fastnn_attend_workspace_size(_desc(**kw), n, 4, m, sel)  # noqa: E731
+    assert size(0, 0) == 256
+    assert size(5, 3) % 256 == 0 and size(5, 3) >= 256
+    # a long table: partial outputs of several splits, 4 bytes an element and a sum a row
+    assert size(2, 1, table_width=4096, heads=1) >= 256 + 2 * 2 * 4 * (64 + 1) * 4
+    assert size(5, 3, sel=-1) == 0 and size(5, 9) == 0
+    assert lib.fastnn_attend_workspace_size(_desc(), 5, 3, 3, 0) == 0
+    assert fnn.fastnn_attend_workspace_size(5, 4, 2, 64, 64, 2, 3, 4, 16) == size(5, 3)
+    assert fnn.fastnn_attend_workspace_size(5, 4, 2, 64, 64, 2, 3, 4, 16, dtype=torch.float32) == 0
+
+
+def test_python_checks():
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    kp, vp, table, lens, cu = z(4, 2, 16, 64), z(4, 2, 16, 64), i(2, 3), i(2), i(3)
+    q = z(5, 4, 64)
+    for bad in (dict(q=z(5, 4, 64, dtype=torch.float32)), dict(v=z(4, 2, 16, 64, dtype=torch.float16))):
+        with pytest.raises(TypeError):
+            fnn.fastnn_attend(bad.get("q", q), kp, bad.get("v", vp), table, lens, cu, 3)
+    for args in ((z(5, 3, 64), kp, vp, table, lens, cu), (q, kp, z(4, 2, 32, 64), table, lens, cu),
+                 (q, kp, vp, table.long(), lens, cu), (q, kp, vp, table, i(3), cu),
+                 (z(5, 4, 128)[:, :, ::2], kp, vp, table, lens, cu), (z(5, 64, 4).transpose(1, 2), kp, vp, table, lens, cu),
+                 (q, kp[:, :, :, :32], vp, table, lens, cu), (q, kp, vp, table, lens, cu)):
+        with pytest.raises(ValueError):  # the last one: not on a CUDA device
+            fnn.fastnn_attend(*args, 3)
+    with pytest.raises(ValueError):
+        fnn.fastnn_attend(q, kp, vp, table, lens, cu, 3, pages=i(5, 4, 2))
+    with pytest.raises(ValueError):
+        fnn.fastnn_rotary(q, i(4), torch.zeros(4, dtype=torch.float64))
+    with pytest.raises(ValueError):
+        fnn.fastnn_rotary(q, i(5), torch.zeros(4))
+    with pytest.raises(ValueError):
+        fnn.fastnn_rotary(q, i(5), torch.zeros(4, dtype=torch.float64), layout="quarter")
+    with pytest.raises(ValueError):
+        fnn.fastnn_store_append(z(5, 2, 64), z(5, 2, 64), kp, vp, table, lens, cu, 3, pos=i(5))
+    with pytest.raises(ValueError):
+        fnn.fastnn_store_append(z(5, 2, 64), z(4, 2, 64), kp, vp, table, lens, cu, 3)
+    with pytest.raises(ValueError):
+        fnn.fastnn_rotary_frequencies(10, axes=2)
+
+
+def test_rotary_frequencies():
+    f = fnn.fastnn_rotary_frequencies(8, base=16.0, stretch=2.0, device="cpu")
+    assert f.dtype == torch.float64 and f.tolist() == [0.5, 0.25, 0.125, 0.0625]
+    assert fnn.fastnn_rotary_frequencies(8, base=16.0, axes=2, device="cpu").tolist() == [1.0, 0.25]
+    assert fnn.fastnn_rotary_frequencies(8, long_base=81.0, device="cpu")[1].item() == pytest.approx(1 / 3)
