@@ -12,7 +12,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfastnn.so")
-SOURCES = ["api.cu", "nn_tc.cu", "l2_nn.cu", "frontier.cu", "noalloc.cu", "rotary.cu", "attend.cu",
+SOURCES = ["api.cu", "nn_tc.cu", "l2_nn.cu", "frontier.cu", "noalloc.cu", "rotary.cu", "attend.cu", "attend_tc.cu",
            "select.cu", "store_api.cu"]
 HEADERS = ["common.cuh", "ptx.cuh", "nn_tc.cuh", "l2_nn.cuh", "frontier.cuh", "frontier_dev.cuh",
            "store.cuh"]

@@ -129,6 +129,13 @@ int launch_store_append(const StoreArgs& a, int dtype, const uint16_t* k, int64_
 // Splits of the few-rows kernel for a call; device-independent.
 void attend_plan(AttendArgs& a);
 int launch_attend_rows(const AttendArgs& a, int dtype, cudaStream_t st);
+// The tensor-core kernel for chunks: which calls it takes (at least kTcRows query
+// rows a sequence and key head; the caller's scale must be positive), and the
+// floats of a.part that it needs.
+constexpr int kTcRows = 64;
+bool attend_tc_takes(const AttendArgs& a);
+size_t attend_tc_floats(const AttendArgs& a);
+int launch_attend_tc(const AttendArgs& a, int dtype, cudaStream_t st);
 int launch_select(const SelectArgs& a, int dtype, cudaStream_t st);
 int select_max_width();
 uint64_t wait_timeout_ns();  // the limit set by fastnn_set_wait_timeout_ns (0: the default)

@@ -110,8 +110,11 @@ int attend_sizes(const fastnn_store* s, int64_t n, int heads_q, int max_new, int
 size_t part_bytes(const AttendArgs& a) {
   return a.splits > 1 ? static_cast<size_t>(a.splits) * a.n * a.hq * sizeof(float) : 0;
 }
+// Either kernel's partial outputs: which one runs also depends on the scale.
 size_t attend_bytes(const AttendArgs& a) {
-  return kAlign + align_up(part_bytes(a) * a.st.dv) + align_up(part_bytes(a));
+  const size_t rows = align_up(part_bytes(a) * a.st.dv) + align_up(part_bytes(a));
+  const size_t tc = attend_tc_takes(a) ? align_up(attend_tc_floats(a) * sizeof(float)) : 0;
+  return kAlign + (rows > tc ? rows : tc);
 }
 
 }  // namespace
@@ -191,6 +194,8 @@ int fastnn_attend(const fastnn_store* store, const void* q, int64_t q_stride, in
   a.part = reinterpret_cast<float*>(ws + kAlign);
   a.part_lse = reinterpret_cast<float*>(ws + kAlign + align_up(part_bytes(a) * a.st.dv));
   a.wait_ns = wait_timeout_ns();
+  if (scale > 0.f && attend_tc_takes(a))
+    return launch_attend_tc(a, store->dtype, reinterpret_cast<cudaStream_t>(stream));
   return launch_attend_rows(a, store->dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 

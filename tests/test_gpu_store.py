@@ -206,15 +206,19 @@ def test_append_reports_tokens_without_a_place(fault):
 
 # ---- attention ---------------------------------------------------------------------------------
 
-def _attend(st, causal=True, scale=None, pages=None, **kw):
+def _attend(st, causal=True, scale=None, pages=None):
     q, kp, vp, table, lens, cu = st.cuda("q", "k_pages", "v_pages", "table", "lens", "cu")
     out = torch.full((st.n, st.heads * st.group, st.dv), 9.0, dtype=st.dtype, device="cuda")
     lse = torch.full((st.n, st.heads * st.group), 9.0, device="cuda")
-    ws = kw.pop("workspace", None)
+    select = 0 if pages is None else pages.shape[2]
+    need = fnn.fastnn_attend_workspace_size(st.n, st.heads * st.group, st.heads, st.d, st.dv, len(st.lens),
+                                            st.max_new, st.width, st.page, select)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
     got = fnn.fastnn_attend(q, kp, vp, table, lens, cu, st.max_new, causal=causal, scale=scale,
                             pages=None if pages is None else pages.cuda(), out=out, lse=lse,
                             workspace=ws)
     assert got[0] is out and got[1] is lse
+    assert fnn.fastnn_device_status(ws) == 0
     end = int(st.cu[-1])
     assert bool((out[end:] == 9).all()) and bool((lse[end:] == 9).all())  # behind the last sequence
     return out, lse
