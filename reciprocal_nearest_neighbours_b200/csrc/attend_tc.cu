@@ -3,10 +3,12 @@
 //
 // The mathematics is that of attend.cu: one pass over the keys with a running
 // maximum and sum. Two things differ. The maximum m that the exponentials
-// refer to is only raised when a tile's maximum is more than 2^kLazy above it,
-// so that O (in tensor memory) is rarely rescaled: weights up to 2^kLazy
-// are as exact in 16-bit floats as weights up to 1, and O / l does not depend
-// on m. And the tiles run from the last key to the first: the tiles with
+// refer to need not be the largest score so far: O / l does not depend on m,
+// and weights up to kMostSum are as exact in 16-bit floats as weights up to 1.
+// So a tile's weights are formed with the m in force, and only if their sum is
+// above kMostSum is the tile's maximum sought, m raised and O (in tensor
+// memory) rescaled. Then the sum of that tile is at most its 128 keys, so m
+// rises by more than 1 each time and soon no more. And the tiles run from the last key to the first: the tiles with
 // masked places come first, the others run unmasked.
 //
 // One CTA per SM, warp-specialised. An item is 2 x 128 query rows (rows are
@@ -54,7 +56,8 @@ constexpr int kOtherRegs = 72;
 constexpr int kBlk = 128;          // rows of a tile (queries, keys)
 constexpr int kItemCost = 2;       // an item's fixed cost, in key tiles
 constexpr int kLeastShare = 4;     // a CTA's share is at least this many tiles
-constexpr float kLazy = 8.f;
+constexpr float kMostSum = 256.f;
+constexpr int kMaxCtas = 160;
 constexpr int kHoleRing = 16;      // tiles whose missing pages are remembered
 
 template <int DP>
@@ -64,7 +67,17 @@ struct Tc {
   static constexpr int kRing = 2 * kTile;          // after the two query tiles
   static constexpr int kCtl = kRing + kStages * kTile;
   static constexpr int kBlock = kBlk * 128;        // bytes of a 64-element column block
+  // Of every 16 pairs of weights, so many by polynomial (12 instructions a pair
+  // against 16 clocks of the special-function unit): where the products are
+  // short, the softmax is what takes the time. Measured with 0 / 2 / 5: 12288
+  // queries over 196608 keys of 24 876 / 805 / 785 us; 2048 over 16384, 32 heads of
+  // 128, 434 / 425 / 432 us.
+  static constexpr int kPolyPairs = DP == 128 ? 2 : 5;
 };
+
+// Tensor memory columns of query tile w: scores at 128 w, the weights over
+// them (packed in pairs, 64 columns), O at 256 + 128 w.
+constexpr uint32_t kOCol = 256;
 
 constexpr int kMaxStages = 8;
 constexpr int kSegRing = 4;        // segments the planning warp is ahead of the others
@@ -88,7 +101,9 @@ struct TcCtl {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
   uint64_t q_full, q_empty, fix, done;
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2];   // scores are there
+  uint64_t p_full[2];   // the weights are there
+  uint64_t o_full[2];   // a segment's last product is complete
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];
   Seg seg[kSegRing];
   uint32_t holes[kHoleRing];
@@ -103,6 +118,14 @@ struct TcArgs {
   int ctas;
   float* part;    // [2 * ctas][256][dv]
   float* part_lse;
+  struct Cut* cuts;  // [ctas]
+};
+
+// Where a CTA's share begins, for the merge.
+struct alignas(16) Cut {
+  int64_t u0, u1;    // the share
+  int64_t base, end; // units of the item that it begins in
+  int s, g, tile, pad;
 };
 
 // ---- the plan: items and shares ------------------------------------------------
@@ -212,6 +235,57 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 halves(uint64_t x) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(x));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// 2^x of two numbers without the special-function unit: x = j + f with j the
+// nearest whole number (the sum with 1.5 * 2^23 leaves it in the low mantissa
+// bits), 2^f by its minimax polynomial of degree 5 on [-1/2, 1/2] (found by
+// Remez exchange on the relative error; in fp32 2^-22.2, as good as the unit's),
+// and j added to the exponent. x <= 8 here; below -126 the result is 2^-126,
+// nothing beside a row's largest weight of at least 2^-8.
+__device__ __forceinline__ float2 ex2_pair(uint64_t x) {
+  float2 v = halves(x);
+  x = pair(fmaxf(v.x, -126.f), fmaxf(v.y, -126.f));
+  const uint64_t magic = pair(12582912.f, 12582912.f);
+  const uint64_t t = add2(x, magic);
+  const uint64_t f = sub2(x, sub2(t, magic));
+  uint64_t q = pair(0.0013276472454890609f, 0.0013276472454890609f);
+  q = fma2(q, f, pair(0.009675540961325169f, 0.009675540961325169f));
+  q = fma2(q, f, pair(0.05550713092088699f, 0.05550713092088699f));
+  q = fma2(q, f, pair(0.24022120237350464f, 0.24022120237350464f));
+  q = fma2(q, f, pair(0.6931469440460205f, 0.6931469440460205f));
+  q = fma2(q, f, pair(1.0000001192092896f, 1.0000001192092896f));
+  const float2 w = halves(q), e = halves(t);
+  return make_float2(__uint_as_float(__float_as_uint(w.x) + (__float_as_uint(e.x) << 23)),
+                     __uint_as_float(__float_as_uint(w.y) + (__float_as_uint(e.y) << 23)));
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
                                             uint32_t bar) {
   asm volatile(
@@ -252,6 +326,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
       "r"(r[30]), "r"(r[31])
       : "memory");
+}
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -343,12 +427,21 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       left = share_start(units, c + 1, ctas) - u;
     }
     if (left > 0) at = locate(p, totals, u, lane);
+    if (lane == 0) {
+      Cut cut{u, u + left, u - at.at, 0, at.s, at.g, at.tile, 0};
+      if (left > 0)
+        cut.end = cut.base + kItemCost +
+                  item_tiles(seq_view(st, at.s, a.n, a.max_new, a.causal), p.tt, at.tile);
+      p.cuts[blockIdx.x] = cut;
+    }
   }
   ptx::fence_proxy_async_smem();  // totals are read; TMA writes there next
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  // The same in every lane, and told so to the compiler: the MMA issuer's
+  // descriptors can then stay in uniform registers.
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
   // Segment k of the share, copied from the ring; false at the end of the
   // share (or when a wait ran out).
   auto segment = [&](int k, Seg& e) {
@@ -365,9 +458,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int w = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + 256 + w * 128;
+    const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + kOCol + w * 128;
     const int nvb = (st.dv + 63) / 64;
-    uint32_t sp = 0, op = 0;
+    const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
+    uint32_t sp = 0, op = 0;  // parities of s_full and o_full
     int tiles = 0;
     Seg e;
     for (int k = 0; segment(k, e); ++k) {
@@ -378,7 +472,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       }
       const int tok = w * p.tt + r / a.group;
       const bool real = r < p.tt * a.group && tok < e.n;
-      const int vis = real ? seg_visible(e, tok) : 0;
+      const int vis = real ? seg_visible(e, tok) : e.vmax;
       const int vmin = __reduce_min_sync(0xffffffffu, vis);
       bool ok = true;
       float m = -INFINITY, l = 0.f;
@@ -388,64 +482,93 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         sp ^= 1;
         if (!ok) break;
         ptx::tc_fence_after();
-        uint32_t x[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(ts + c * 32, x[c]);
         const uint32_t holes = ctl->holes[tiles & (kHoleRing - 1)];
-        ptx::tmem_ld_wait();
+        const bool edge = k0 + kBlk > vmin || holes;
+        uint32_t x[4][32];
+        uint32_t pk[4][16];
+        auto load = [&]() {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::pin_regs(x[c]);
-        if (k0 + kBlk > vmin || holes) {
+          for (int c = 0; c < 4; ++c) ptx::tmem_ld32(ts + c * 32, x[c]);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) ptx::pin_regs(x[c]);
+        };
+        // The weights with the maximum in force, packed; returns their sum.
+        auto weigh = [&](auto poly) {
+          const float z = m == -INFINITY ? 0.f : -m;
+          const uint64_t z2 = pair(z, z);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int key = c * 32 + i;
-              if (k0 + key >= vis || ((holes >> (key >> st.page_log2)) & 1u))
-                x[c][i] = __float_as_uint(-INFINITY);
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t u = fma2(pair(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])),
+                                      scale2, z2);
+              float2 v;
+              if (i < decltype(poly)::value) {
+                v = ex2_pair(u);
+              } else {
+                v = halves(u);
+                v = make_float2(ex2(v.x), ex2(v.y));
+              }
+              sum[i & 1] = add2(sum[i & 1], pair(v.x, v.y));
+              pk[c][i] = Half16<T>::pack(v.x, v.y);
             }
+          const float2 y = halves(add2(sum[0], sum[1]));
+          return y.x + y.y;
+        };
+        load();
+        // Most tiles need no maximum of their own: while their weights, by the
+        // maximum in force, sum to no more than kMostSum, none of them is larger.
+        float sum = 0.f;
+        bool again = edge || t == 0;
+        if (!again) {
+          sum = weigh(std::integral_constant<int, C::kPolyPairs>{});
+          again = __any_sync(0xffffffffu, sum > kMostSum || m == -INFINITY);
         }
-        float top[4];
+        if (again) {
+          load();  // the scores are still there: the weights have not been stored
+          if (edge) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          top[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 2; i < 32; i += 2)
-            top[c] = ptx::fmax3(top[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-        }
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-        if (__any_sync(0xffffffffu, mx > m + kLazy || (m == -INFINITY && mx > m))) {
-          const float up = fmaxf(m, mx);
-          const float f = m == up ? 1.f : ex2(m - up);
-          l *= f;
-          m = up;
-          if (t > 0) {
-            for (int c = 0; c < nvb * 2; ++c) {
-              uint32_t o[32];
-              ptx::tmem_ld32(to + c * 32, o);
-              ptx::tmem_ld_wait_regs(o);
+              for (int i = 0; i < 32; ++i) {
+                const int key = c * 32 + i;
+                if (k0 + key >= vis || ((holes >> (key >> st.page_log2)) & 1u))
+                  x[c][i] = __float_as_uint(-INFINITY);
+              }
+          }
+          float top[4];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(to + c * 32, o);
+          for (int c = 0; c < 4; ++c) {
+            top[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
+#pragma unroll
+            for (int i = 2; i < 32; i += 2)
+              top[c] = ptx::fmax3(top[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+          }
+          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+          if (__any_sync(0xffffffffu, mx > m)) {
+            // Raise the maximum, and scale what was summed with the one before.
+            const float up = fmaxf(m, mx);
+            const float f = m == up ? 1.f : ex2(m - up);
+            l *= f;
+            m = up;
+            if (t > 0) {
+              for (int c = 0; c < nvb * 2; ++c) {
+                uint32_t o[32];
+                ptx::tmem_ld32(to + c * 32, o);
+                ptx::tmem_ld_wait_regs(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(to + c * 32, o);
+              }
             }
           }
+          sum = weigh(std::integral_constant<int, 0>{});
         }
-        const float z = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {};
+        l += sum;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float u = ex2(fmaf(__uint_as_float(x[c][2 * i]), a.scale_log2, z));
-            const float v = ex2(fmaf(__uint_as_float(x[c][2 * i + 1]), a.scale_log2, z));
-            sum[(2 * i) & 3] += u;
-            sum[(2 * i + 1) & 3] += v;
-            pk[i] = Half16<T>::pack(u, v);
-          }
-          tmem_st16(ts + c * 16, pk);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        for (int c = 0; c < 4; ++c) tmem_st16(ts + c * 16, pk[c]);
         tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
@@ -519,15 +642,19 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                           e.tok + q * p.tt, bar(ctl->q_full));
         }
         ++segs;
-        for (int j = e.jb - 1; j >= e.ja; --j, ++tiles) {
-          // Lane i < ppt has the tile's page i; -1: no such page, or none of its
-          // positions is visible.
-          int id = -1;
+        // Lane i < ppt has page i of a tile; -1: no such page, or none of its
+        // positions is visible. Read a tile ahead.
+        auto page_id = [&](int j) {
           const int lp = (j << p.ppt_log2) + lane;
-          if (lane < ppt && lp < st.width && (lp << st.page_log2) < vmax) {
-            id = __ldg(st.table + static_cast<int64_t>(e.s) * st.width + lp);
-            if (id >= st.n_pages) id = -1;
-          }
+          return j >= e.ja && lane < ppt && lp < st.width && (lp << st.page_log2) < vmax
+                     ? __ldg(st.table + static_cast<int64_t>(e.s) * st.width + lp)
+                     : -1;
+        };
+        int id_next = page_id(e.jb - 1);
+        for (int j = e.jb - 1; j >= e.ja; --j, ++tiles) {
+          int id = id_next;
+          if (id >= st.n_pages) id = -1;
+          id_next = page_id(j - 1);
           const unsigned there = __ballot_sync(0xffffffffu, lane < ppt && id >= 0);
           const unsigned every = ppt == 32 ? 0xffffffffu : (1u << ppt) - 1u;
           const bool fix = there != every || (j + 1) * kBlk > vmax;
@@ -556,12 +683,13 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 break;
               }
               fix_phase ^= 1;
-              for (int r = 0; r < kBlk; ++r) {
-                const bool real = j * kBlk + r < vmax && ((there >> (r >> st.page_log2)) & 1u);
-                if (real) continue;
-                for (int i = lane; i < blocks * 32; i += 32)
-                  *reinterpret_cast<uint32_t*>(smem + C::kRing + stage * C::kTile +
-                                               (i >> 5) * C::kBlock + r * 128 + (i & 31) * 4) = 0;
+              // Four rows of 128 bytes at a time, 16 bytes a lane.
+              const int from = there == every ? (vmax > j * kBlk ? vmax - j * kBlk : 0) : 0;
+              for (int r = (from & ~3) + (lane >> 3); r < kBlk; r += 4) {
+                if (j * kBlk + r < vmax && ((there >> (r >> st.page_log2)) & 1u)) continue;
+                for (int b = 0; b < blocks; ++b)
+                  *reinterpret_cast<uint4*>(smem + C::kRing + stage * C::kTile + b * C::kBlock + r * 128 +
+                                            (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
               }
               ptx::fence_proxy_async_smem();
               __syncwarp();
@@ -597,7 +725,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           }
       }
     } else if (warp == kMmaWarp) {
-      // The whole warp waits; lane 0 issues.
+      // The whole warp waits; one elected lane issues.
+      const bool leader = elect_one();
       constexpr uint32_t kFmt = std::is_same<T, __half>::value ? 0u : 1u;
       const uint32_t nvb = (st.dv + 63) / 64;
       const uint32_t idesc_s = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
@@ -623,9 +752,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       };
       auto product_o = [&](int w, int vstage, bool fresh) {
         const uint64_t vd = smem_desc_mn(sbase + C::kRing + vstage * C::kTile, C::kBlock);
-  #pragma unroll
+#pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8, vd + ks * (2048 >> 4), idesc_o,
+          mma_ts(tmem + kOCol + w * 128, tmem + w * 128 + ks * 8, vd + ks * (2048 >> 4), idesc_o,
                  (fresh && ks == 0) ? 0u : 1u);
       };
       auto step = [&]() {
@@ -639,27 +768,24 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         const int nw = p.tt < e.n ? 2 : 1, nt = e.jb - e.ja;
         if (!await(ctl->q_full, k & 1) || !await(ctl->full[stage], phase)) break;
         ptx::tc_fence_after();
-        if (lane == 0) {
+        if (leader) {
           for (int w = 0; w < nw; ++w) product_s(w, stage);
           ptx::mma_commit(bar(ctl->empty[stage]));
           if (nt == 1) ptx::mma_commit(bar(ctl->q_empty));
         }
         step();
         bool ok = true;
-        for (int t = 0; t < nt && ok; ++t) {
-          ok = await(ctl->full[stage], phase);
-          if (!ok) break;
+        for (int t = 0; t < nt; ++t) {
+          if (!(ok = await(ctl->full[stage], phase))) break;
           const int vstage = stage;
           step();
           const bool more = t + 1 < nt;
-          if (more) ok = await(ctl->full[stage], phase);
-          if (!ok) break;
+          if (more && !(ok = await(ctl->full[stage], phase))) break;
           for (int w = 0; w < nw; ++w) {
-            ok = await(ctl->p_full[w], (pp >> w) & 1u);
+            if (!(ok = await(ctl->p_full[w], (pp >> w) & 1u))) break;
             pp ^= 1u << w;
-            if (!ok) break;
             ptx::tc_fence_after();
-            if (lane == 0) {
+            if (leader) {
               product_o(w, vstage, t == 0);
               if (more) {
                 product_s(w, stage);
@@ -669,7 +795,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             }
           }
           if (!ok) break;
-          if (lane == 0) {
+          if (leader) {
             ptx::mma_commit(bar(ctl->empty[vstage]));
             if (more) {
               ptx::mma_commit(bar(ctl->empty[stage]));
@@ -681,7 +807,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         if (!ok) break;
       }
       // Everything issued is complete before the tensor memory goes back.
-      if (lane == 0) {
+      if (leader) {
         ptx::mma_commit(bar(ctl->done));
         const uint64_t t0 = ptx::globaltimer_ns();
         while (!ptx::mbar_try_wait(bar(ctl->done), 0) && ptx::globaltimer_ns() - t0 < kTimeoutNs) {
@@ -752,41 +878,36 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 }
 
 // Joins the partial outputs of the items that a share's border divides. Block
-// (c, i) looks at the border before CTA c and takes every gridDim.y-th group
+// (c, i) looks at the border before CTA c + 1 and takes every gridDim.y-th group
 // of rows of its item, if the item's first cut is there.
 template <typename T>
 __global__ void __launch_bounds__(256)
 merge_kernel(const __grid_constant__ TcArgs p) {
-  extern __shared__ int64_t totals[];
-  __shared__ Spot spot;
+  cudaGridDependencySynchronize();
   const AttendArgs& a = p.a;
   const StoreArgs& st = a.st;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ctas = plan(p, totals, warp, 8, lane);
-  const int c = blockIdx.x + 1;
-  if (c >= ctas) return;
-  const int64_t units = totals[st.n_seqs - 1];
-  const int64_t u = share_start(units, c, ctas);
-  if (warp == 0) {
-    const Spot sp = locate(p, totals, u, lane);
-    if (lane == 0) spot = sp;
-  }
+  const int c = blockIdx.x + 1, ctas = p.ctas;
+  __shared__ Cut cuts[kMaxCtas];
+  const Cut sp = p.cuts[c];
+  if (sp.u0 >= sp.u1 || sp.u0 == sp.base || p.cuts[c - 1].u0 > sp.base) return;
+  for (int i = threadIdx.x; i < ctas * static_cast<int>(sizeof(Cut) / 16); i += 256)
+    reinterpret_cast<int4*>(cuts)[i] = reinterpret_cast<const int4*>(p.cuts)[i];
   __syncthreads();
-  const Spot sp = spot;
-  const int64_t base = u - sp.at;  // the item's first unit
-  if (sp.at == 0 || share_start(units, c - 1, ctas) > base) return;
-  const SeqView w = seq_view(st, sp.s, a.n, a.max_new, a.causal);
-  const int kt = item_tiles(w, p.tt, sp.tile);
-  const int64_t end = base + kt + kItemCost;
+  const int64_t base = sp.base, end = sp.end;
   // The CTAs c - 1 .. last have a part each, but for those without a tile.
+  auto has_part = [&](const Cut& k) {
+    return tiles_of((k.u1 < end ? k.u1 : end) - base) > tiles_of(k.u0 > base ? k.u0 - base : 0);
+  };
   int parts = 0, last = c - 1;
   for (int k = c - 1; k < ctas; ++k) {
-    const int64_t s0 = share_start(units, k, ctas), s1 = share_start(units, k + 1, ctas);
-    if (s0 >= end) break;
-    parts += tiles_of((s1 < end ? s1 : end) - base) > tiles_of(s0 > base ? s0 - base : 0);
+    const Cut& cut = cuts[k];
+    if (cut.u0 >= end || cut.u0 >= cut.u1) break;
+    parts += has_part(cut);
     last = k;
   }
   if (parts <= 1) return;
+  const SeqView w = seq_view(st, sp.s, a.n, a.max_new, a.causal);
   const int i0 = sp.tile * 2 * p.tt;
   for (int rr = blockIdx.y * 8 + warp; rr < 256; rr += gridDim.y * 8) {
     const int q = rr >> 7, r = rr & 127;
@@ -797,9 +918,9 @@ merge_kernel(const __grid_constant__ TcArgs p) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int pass = 0; pass < 2; ++pass) {
       for (int k = c - 1; k <= last; ++k) {
-        const int64_t s0 = share_start(units, k, ctas), s1 = share_start(units, k + 1, ctas);
-        if (tiles_of((s1 < end ? s1 : end) - base) <= tiles_of(s0 > base ? s0 - base : 0)) continue;
-        const int slot = 2 * k + (s0 < base ? 1 : 0);
+        const Cut& cut = cuts[k];
+        if (!has_part(cut)) continue;
+        const int slot = 2 * k + (cut.u0 < base ? 1 : 0);
         const float z = p.part_lse[slot * 256 + rr];
         if (pass == 0) {
           top = fmaxf(top, z);
@@ -862,7 +983,6 @@ int make_map(CUtensorMap* m, bool bf16, const void* base, uint64_t n0, uint64_t 
   return r == CUDA_SUCCESS ? FASTNN_OK : FASTNN_ERR_CUDA;
 }
 
-constexpr int kMaxCtas = 160;
 constexpr int kMaxSeqs = 512;  // of one launch: the plan's sums fit beside the queries
 
 template <typename T, int DP>
@@ -882,6 +1002,7 @@ int tc_launch(const AttendArgs& all, cudaStream_t stream) {
   p.ctas = sms < kMaxCtas ? sms : kMaxCtas;
   p.part = all.part;
   p.part_lse = all.part + static_cast<int64_t>(2) * kMaxCtas * 256 * all.st.dv;
+  p.cuts = reinterpret_cast<Cut*>(p.part_lse + 2 * kMaxCtas * 256);
   const StoreArgs& st = all.st;
   CUtensorMap qm, km, vm;
   int e = make_map(&qm, bf16, all.q, st.d, all.hq, all.n, st.d, all.q_stride, all.group, p.tt);
@@ -903,8 +1024,7 @@ int tc_launch(const AttendArgs& all, cudaStream_t stream) {
     q.a.st.cu += s0;
     attend_tc_kernel<T, DP><<<p.ctas, kThreads, kSmem, stream>>>(qm, km, vm, q);
     FASTNN_CUDA_TRY(cudaGetLastError());
-    merge_kernel<T><<<dim3(p.ctas - 1, 4), 256, q.a.st.n_seqs * sizeof(int64_t), stream>>>(q);
-    FASTNN_CUDA_TRY(cudaGetLastError());
+    FASTNN_CUDA_TRY(launch_after(merge_kernel<T>, dim3(p.ctas - 1, 16), dim3(256), stream, q));
   }
   return FASTNN_OK;
 }
@@ -923,7 +1043,7 @@ bool attend_tc_takes(const AttendArgs& a) {
 }
 
 size_t attend_tc_floats(const AttendArgs& a) {
-  return static_cast<size_t>(2) * kMaxCtas * 256 * (a.st.dv + 1);
+  return static_cast<size_t>(2) * kMaxCtas * 256 * (a.st.dv + 1) + kMaxCtas * sizeof(Cut) / sizeof(float);
 }
 
 int launch_attend_tc(const AttendArgs& a, int dtype, cudaStream_t st) {
