@@ -388,7 +388,8 @@ int fastnn_rotary(const void *x, int64_t x_stride, int64_t n, int heads, int d,
  *   A new token that has no place (a hole, or a position past the table) is
  *   not stored; fastnn_device_status() then reports FASTNN_ERR_INVALID, as it
  *   does for a sequence with a negative length or more than max_new tokens.
- *   workspace: FASTNN_STORE_APPEND_WORKSPACE bytes. n == 0 is a no-op.
+ *   workspace: FASTNN_STORE_APPEND_WORKSPACE bytes for that report, or NULL
+ *   (nothing is reported). n == 0 is a no-op.
  */
 #define FASTNN_STORE_APPEND_WORKSPACE 256
 int fastnn_store_append(const fastnn_store *store, const void *k, int64_t k_stride,
@@ -440,7 +441,8 @@ int fastnn_attend(const fastnn_store *store, const void *q, int64_t q_stride, in
  *   be NULL); dv is not used but must be valid.
  *   workspace: fastnn_select_workspace_size() bytes, 256-byte aligned.
  */
-size_t fastnn_select_workspace_size(const fastnn_store *store, int64_t n);
+size_t fastnn_select_workspace_size(const fastnn_store *store, int64_t n, int heads_q,
+                                    int max_new);
 int fastnn_select_pages(const fastnn_store *store, const void *q, int64_t q_stride,
                         int64_t n, int heads_q, int max_new, int causal, int keep_first,
                         int keep_last, int select, int32_t *out_pages, void *workspace,

@@ -17,11 +17,11 @@ others:
 from __future__ import annotations
 
 import ctypes
-import math
+import struct
 
 import torch
 
-from ._lib import FASTNN_BF16, FASTNN_F16, FastNNError, _check, library
+from ._lib import FASTNN_BF16, FASTNN_F16, FastNNError, library
 
 FASTNN_ROTARY_HALF = 0
 FASTNN_ROTARY_INTERLEAVED = 1
@@ -31,21 +31,13 @@ _LAYOUTS = {"half": FASTNN_ROTARY_HALF, "interleaved": FASTNN_ROTARY_INTERLEAVED
 _CODES = {torch.bfloat16: FASTNN_BF16, torch.float16: FASTNN_F16}
 
 
-class _Store(ctypes.Structure):
-    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
-                ("k_mean", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
-                ("lens", ctypes.c_void_p), ("cu", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
-                ("n_seqs", ctypes.c_int), ("table_width", ctypes.c_int), ("page", ctypes.c_int),
-                ("heads", ctypes.c_int), ("d", ctypes.c_int), ("dv", ctypes.c_int),
-                ("dtype", ctypes.c_int)]
-
-
-class _Rotation(ctypes.Structure):
-    _fields_ = [("pos", ctypes.c_void_p), ("freq", ctypes.c_void_p), ("axes", ctypes.c_int),
-                ("rot", ctypes.c_int), ("layout", ctypes.c_int), ("scale", ctypes.c_float)]
-
+# fastnn_store and fastnn_rotation, packed as the C compiler lays them out (a call passes
+# the bytes: cheaper than filling a ctypes structure field by field).
+_STORE = struct.Struct("@PPPPPPqiiiiiii")
+_ROTATION = struct.Struct("@PPiiif")
 
 _bound = None
+_I32 = torch.int32
 
 
 def _lib():
@@ -53,14 +45,14 @@ def _lib():
     if _bound is None:
         lib = library()
         P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
-        S, R, F = ctypes.POINTER(_Store), ctypes.POINTER(_Rotation), ctypes.c_float
+        B, F = ctypes.c_char_p, ctypes.c_float
         for name, args, res in (
-                ("fastnn_rotary", [P, I64, I64, I, I, I, R, I, P, I64, P], I),
-                ("fastnn_store_append", [S, P, I64, P, I64, I64, I, R, P, SZ, P], I),
-                ("fastnn_attend_workspace_size", [S, I64, I, I, I], SZ),
-                ("fastnn_attend", [S, P, I64, I64, I, I, I, F, P, I, P, P, P, SZ, P], I),
-                ("fastnn_select_workspace_size", [S, I64], SZ),
-                ("fastnn_select_pages", [S, P, I64, I64, I, I, I, I, I, I, P, P, SZ, P], I)):
+                ("fastnn_rotary", [P, I64, I64, I, I, I, B, I, P, I64, P], I),
+                ("fastnn_store_append", [B, P, I64, P, I64, I64, I, B, P, SZ, P], I),
+                ("fastnn_attend_workspace_size", [B, I64, I, I, I], SZ),
+                ("fastnn_attend", [B, P, I64, I64, I, I, I, F, P, I, P, P, P, SZ, P], I),
+                ("fastnn_select_workspace_size", [B, I64, I, I], SZ),
+                ("fastnn_select_pages", [B, P, I64, I64, I, I, I, I, I, I, P, P, SZ, P], I)):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, res
         _bound = lib
@@ -74,74 +66,82 @@ def _code(t: torch.Tensor) -> int:
     return code
 
 
-def _rows(t: torch.Tensor, what: str, heads: int, d: int) -> int:
+def _rows(t: torch.Tensor, what: str, n: int, heads: int, d: int) -> int:
     """Token stride of ``t`` [n, heads, d], whose heads lie one after the other."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{what} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
+    if t.shape != (n, heads, d):
+        raise ValueError(f"{what} must be [{n}, {heads}, {d}], got {tuple(t.shape)}")
     stride, head, one = t.stride()
-    if t.shape[0] < 2:
+    if n < 2:
         stride = max(stride, heads * d)
     if (one != 1 and d > 1) or (head != d and heads > 1) or stride < heads * d:
         raise ValueError(f"{what}: the heads of a token must lie one after the other")
     return stride
 
 
-def _index(t: torch.Tensor, what: str, dims: int, dev):
-    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
+def _index(t: torch.Tensor, what: str, dims: int, dev: int) -> int:
+    """Address of an int32 index array."""
+    if t.dtype is not _I32 or t.dim() != dims or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of {dims} dimension(s)")
-    if t.device != dev:
-        raise ValueError(f"{what} is on {t.device}, the tokens on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the tokens on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _same(dev, dtype, **tensors):
-    for what, t in tensors.items():
-        if t.device != dev:
-            raise ValueError(f"{what} is on {t.device}, the tokens on {dev}")
-        if t.dtype != dtype:
-            raise TypeError(f"{what} is {t.dtype}, the tokens {dtype}")
+def _same(dev: int, dtype, what: str, t: torch.Tensor) -> int:
+    """Address of ``t``, which must be of the tokens' device and type."""
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the tokens on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} is {t.dtype}, the tokens {dtype}")
+    return t.data_ptr()
 
 
-class _On:
-    """The tensors' device as the current one, and the stream to launch on."""
+def _device(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    return t.get_device()
 
-    def __init__(self, dev, stream):
-        if dev.type != "cuda":
-            raise ValueError("tensors must be CUDA tensors")
-        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        if s.device != dev:
-            raise ValueError(f"the stream is on {s.device}, the tokens on {dev}")
-        self.stream = s.cuda_stream
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _launch(what: str, dev: int, stream, *args):
+    """Call the library with the tensors' device current, on ``stream`` (None: the device's
+    current one)."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tokens on cuda:{dev}")
+        raw = stream.cuda_stream
+    fn = getattr(_bound, what)
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, raw)
+    if rc:
+        raise FastNNError(rc, what)
 
 
 def _describe(code, dev, page_table, lens, cu, n_pages, heads, page, d, dv, k=None, v=None,
-              mean=None) -> _Store:
-    _index(page_table, "page_table", 2, dev)
-    _index(lens, "lens", 1, dev)
-    _index(cu, "cu", 1, dev)
+              mean=None) -> bytes:
+    t, n, c = (_index(page_table, "page_table", 2, dev), _index(lens, "lens", 1, dev),
+               _index(cu, "cu", 1, dev))
     seqs, width = page_table.shape
     if lens.shape[0] != seqs or cu.shape[0] != seqs + 1:
         raise ValueError("page_table [n_seqs, width], lens [n_seqs] and cu [n_seqs + 1] disagree")
-    return _Store(k, v, mean, page_table.data_ptr(), lens.data_ptr(), cu.data_ptr(), n_pages, seqs,
-                  width, page, heads, d, dv, code)
+    return _STORE.pack(k or 0, v or 0, mean or 0, t, n, c, n_pages, seqs, width, page, heads, d, dv,
+                       code)
 
 
-def _pages(k_pages, v_pages):
-    if k_pages.dim() != 4 or v_pages.dim() != 4 or k_pages.shape[:3] != v_pages.shape[:3]:
+def _pages(k_pages, v_pages, dev, dtype):
+    """Shape [n_pages, heads, page, d], dv, and the addresses of both."""
+    kp, vp = _same(dev, dtype, "k_pages", k_pages), _same(dev, dtype, "v_pages", v_pages)
+    shape, other = k_pages.shape, v_pages.shape
+    if len(shape) != 4 or len(other) != 4 or shape[:3] != other[:3]:
         raise ValueError("k_pages [n_pages, heads, page, d] and v_pages [n_pages, heads, page, dv] "
-                         f"disagree: {tuple(k_pages.shape)}, {tuple(v_pages.shape)}")
+                         f"disagree: {tuple(shape)}, {tuple(other)}")
     if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("k_pages and v_pages must be contiguous")
-    return k_pages.shape
+    return shape, other[3], kp, vp
 
 
 def _new(shape, dtype, dev, stream):
@@ -154,32 +154,32 @@ def _new(shape, dtype, dev, stream):
 
 
 def _scratch(need: int, dev, workspace, what: str, stream):
+    """The call's workspace and its size."""
     if need == 0:
         raise FastNNError(-1, what)
     if workspace is None:
         return _new(need, torch.uint8, dev, stream)
-    if workspace.device != dev:
-        raise ValueError(f"the workspace is on {workspace.device}, the tokens on {dev}")
+    if workspace.get_device() != dev:
+        raise ValueError(f"the workspace is on {workspace.device}, the tokens on cuda:{dev}")
     if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
         raise FastNNError(-3, "workspace")
     return workspace
 
 
-def _rotation(pos, freq, layout, scale, n, dev) -> _Rotation:
-    if layout not in _LAYOUTS:
+def _rotation(pos, freq, layout, scale, n, dev) -> bytes:
+    code = _LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
-    if pos.dim() == 1:
-        pos = pos.unsqueeze(1)
-    _index(pos, "pos", 2, dev)
-    if freq.dtype != torch.float64 or freq.dim() != 1 or not freq.is_contiguous() or \
-            freq.device != dev:
-        raise ValueError(f"freq must be a contiguous float64 vector on {dev}")
-    axes = pos.shape[1]
+    dims = pos.dim()
+    at = _index(pos, "pos", 1 if dims == 1 else 2, dev)
+    if freq.dtype is not torch.float64 or freq.dim() != 1 or not freq.is_contiguous() or \
+            freq.get_device() != dev:
+        raise ValueError(f"freq must be a contiguous float64 vector on cuda:{dev}")
+    axes = 1 if dims == 1 else pos.shape[1]
     if pos.shape[0] != n or axes not in (1, 2):
         raise ValueError(f"pos must be [tokens] or [tokens, 1 or 2] for {n} tokens, "
                          f"got {tuple(pos.shape)}")
-    return _Rotation(pos.data_ptr(), freq.data_ptr(), axes, 2 * axes * freq.shape[0],
-                     _LAYOUTS[layout], scale)
+    return _ROTATION.pack(at, freq.data_ptr(), axes, 2 * axes * freq.shape[0], code, scale)
 
 
 def fastnn_rotary_frequencies(rot: int, base: float = 10000.0, axes: int = 1, stretch: float = 1.0,
@@ -211,22 +211,17 @@ def fastnn_rotary(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, layout
     code = _code(x)
     if x.dim() != 3:
         raise ValueError(f"x must be [tokens, heads, d], got {tuple(x.shape)}")
+    dev = _device(x)
     n, heads, d = x.shape
-    dev = x.device
-    xs = _rows(x, "x", heads, d)
+    xs = _rows(x, "x", n, heads, d)
     rot = _rotation(pos, freq, layout, scale, n, dev)
     if out is None:
         out = _new((n, heads, d), x.dtype, dev, stream)
-        os = heads * d
+        to, os = out.data_ptr(), heads * d
     else:
-        _same(dev, x.dtype, out=out)
-        if out.shape != x.shape:
-            raise ValueError(f"out must be {tuple(x.shape)}, got {tuple(out.shape)}")
-        os = _rows(out, "out", heads, d)
-    with _On(dev, stream) as st:
-        rc = _lib().fastnn_rotary(x.data_ptr(), xs, n, heads, d, code, rot, int(inverse),
-                                  out.data_ptr(), os, st)
-    _check(rc, "fastnn_rotary")
+        to, os = _same(dev, x.dtype, "out", out), _rows(out, "out", n, heads, d)
+    _bound or _lib()
+    _launch("fastnn_rotary", dev, stream, x.data_ptr(), xs, n, heads, d, code, rot, inverse, to, os)
     return out
 
 
@@ -239,42 +234,39 @@ def fastnn_store_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
     Token i of sequence s becomes position ``lens[s] + i``; ``lens`` itself is the
     caller's to advance. ``pos`` and ``freq`` (both or neither) rotate the keys on the
     way, as ``fastnn_rotary`` does. ``k_mean`` [n_pages, heads, d] receives the mean key
-    of every page that the call touches. ``fastnn_device_status(workspace)`` tells
-    whether each token found a place.
+    of every page that the call touches. With a ``workspace`` (256 bytes),
+    ``fastnn_device_status(workspace)`` tells whether each token found a place.
     """
     code = _code(k)
-    n_pages, heads, page, d = _pages(k_pages, v_pages)
-    dv = v_pages.shape[3]
-    dev = k.device
-    _same(dev, k.dtype, v=v, k_pages=k_pages, v_pages=v_pages)
-    ks, vs = _rows(k, "k", heads, d), _rows(v, "v", heads, dv)
+    dev = _device(k)
+    dtype = k.dtype
+    (n_pages, heads, page, d), dv, kp, vp = _pages(k_pages, v_pages, dev, dtype)
     n = k.shape[0]
-    if v.shape[0] != n:
-        raise ValueError(f"k has {n} tokens, v {v.shape[0]}")
+    ks, vs = _rows(k, "k", n, heads, d), _rows(v, "v", n, heads, dv)
+    at_v = _same(dev, dtype, "v", v)
     mean = None
     if k_mean is not None:
-        _same(dev, k.dtype, k_mean=k_mean)
+        mean = _same(dev, dtype, "k_mean", k_mean)
         if k_mean.shape != (n_pages, heads, d) or not k_mean.is_contiguous():
             raise ValueError(f"k_mean must be contiguous [{n_pages}, {heads}, {d}]")
-        mean = k_mean.data_ptr()
-    store = _describe(code, dev, page_table, lens, cu, n_pages, heads, page, d, dv,
-                      k_pages.data_ptr(), v_pages.data_ptr(), mean)
+    store = _describe(code, dev, page_table, lens, cu, n_pages, heads, page, d, dv, kp, vp, mean)
     if (pos is None) != (freq is None):
         raise ValueError("pos and freq come together")
     rot = None if pos is None else _rotation(pos, freq, layout, scale, n, dev)
-    ws = _scratch(FASTNN_STORE_APPEND_WORKSPACE, dev, workspace, "fastnn_store_append", stream)
-    with _On(dev, stream) as st:
-        rc = _lib().fastnn_store_append(store, k.data_ptr(), ks, v.data_ptr(), vs, n, max_new, rot,
-                                        ws.data_ptr(), FASTNN_STORE_APPEND_WORKSPACE, st)
-    _check(rc, "fastnn_store_append")
+    ws = None
+    if workspace is not None:
+        ws = _scratch(FASTNN_STORE_APPEND_WORKSPACE, dev, workspace, "", stream).data_ptr()
+    _bound or _lib()
+    _launch("fastnn_store_append", dev, stream, store, k.data_ptr(), ks, at_v, vs, n, max_new, rot,
+            ws, FASTNN_STORE_APPEND_WORKSPACE)
 
 
 def fastnn_attend_workspace_size(n: int, heads_q: int, heads: int, d: int, dv: int, n_seqs: int,
                                  max_new: int, table_width: int, page: int, select: int = 0,
                                  dtype: torch.dtype = torch.bfloat16) -> int:
     """Workspace bytes of ``fastnn_attend`` for these sizes (0: no call would accept them)."""
-    store = _Store(None, None, None, None, None, None, 1, n_seqs, table_width, page, heads, d, dv,
-                   _CODES.get(dtype, -1))
+    store = _STORE.pack(0, 0, 0, 0, 0, 0, 1, n_seqs, table_width, page, heads, d, dv,
+                        _CODES.get(dtype, -1))
     return int(_lib().fastnn_attend_workspace_size(store, n, heads_q, max_new, select))
 
 
@@ -292,42 +284,37 @@ def fastnn_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     and -inf.
     """
     code = _code(q)
-    n_pages, heads, page, d = _pages(k_pages, v_pages)
-    dv = v_pages.shape[3]
-    dev = q.device
-    _same(dev, q.dtype, k_pages=k_pages, v_pages=v_pages)
-    if q.dim() != 3 or q.shape[1] % heads:
+    dev = _device(q)
+    dtype = q.dtype
+    (n_pages, heads, page, d), dv, kp, vp = _pages(k_pages, v_pages, dev, dtype)
+    if q.dim() != 3 or heads < 1 or q.shape[1] % heads:
         raise ValueError(f"q must be [tokens, a multiple of {heads}, {d}], got {tuple(q.shape)}")
-    n, hq = q.shape[0], q.shape[1]
-    qs = _rows(q, "q", hq, d)
-    store = _describe(code, dev, page_table, lens, cu, n_pages, heads, page, d, dv,
-                      k_pages.data_ptr(), v_pages.data_ptr())
+    n, hq, _ = q.shape
+    qs = _rows(q, "q", n, hq, d)
+    store = _describe(code, dev, page_table, lens, cu, n_pages, heads, page, d, dv, kp, vp)
     select, listed = 0, None
     if pages is not None:
-        _index(pages, "pages", 3, dev)
+        listed = _index(pages, "pages", 3, dev)
         if pages.shape[0] != n or pages.shape[1] != heads or pages.shape[2] < 1:
             raise ValueError(f"pages must be [{n}, {heads}, select], got {tuple(pages.shape)}")
-        select, listed = pages.shape[2], pages.data_ptr()
+        select = pages.shape[2]
     if out is None:
-        out = _new((n, hq, dv), q.dtype, dev, stream)
+        out = _new((n, hq, dv), dtype, dev, stream)
     else:
-        _same(dev, q.dtype, out=out)
+        _same(dev, dtype, "out", out)
         if out.shape != (n, hq, dv) or not out.is_contiguous():
             raise ValueError(f"out must be contiguous [{n}, {hq}, {dv}]")
     if lse is None:
         lse = _new((n, hq), torch.float32, dev, stream)
     else:
-        _same(dev, torch.float32, lse=lse)
+        _same(dev, torch.float32, "lse", lse)
         if lse.shape != (n, hq) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous [{n}, {hq}]")
-    lib = _lib()
-    need = lib.fastnn_attend_workspace_size(store, n, hq, max_new, select)
+    need = (_bound or _lib()).fastnn_attend_workspace_size(store, n, hq, max_new, select)
     ws = _scratch(need, dev, workspace, "fastnn_attend_workspace_size", stream)
-    with _On(dev, stream) as st:
-        rc = lib.fastnn_attend(store, q.data_ptr(), qs, n, hq, max_new, int(causal),
-                               1.0 / math.sqrt(d) if scale is None else scale, listed, select,
-                               out.data_ptr(), lse.data_ptr(), ws.data_ptr(), need, st)
-    _check(rc, "fastnn_attend")
+    _launch("fastnn_attend", dev, stream, store, q.data_ptr(), qs, n, hq, max_new, causal,
+            d ** -0.5 if scale is None else scale, listed, select, out.data_ptr(), lse.data_ptr(),
+            ws.data_ptr(), need)
     return out, lse
 
 
@@ -343,29 +330,24 @@ def fastnn_select_pages(q: torch.Tensor, k_mean: torch.Tensor, page_table: torch
     select]: logical page numbers in ascending order, -1 behind the last.
     """
     code = _code(q)
-    dev = q.device
-    _same(dev, q.dtype, k_mean=k_mean)
+    dev = _device(q)
+    mean = _same(dev, q.dtype, "k_mean", k_mean)
     if k_mean.dim() != 3 or not k_mean.is_contiguous():
         raise ValueError("k_mean must be contiguous [n_pages, heads, d]")
     n_pages, heads, d = k_mean.shape
     if q.dim() != 3 or heads < 1 or q.shape[1] % heads:
         raise ValueError(f"q must be [tokens, a multiple of {heads}, {d}], got {tuple(q.shape)}")
-    n, hq = q.shape[0], q.shape[1]
-    qs = _rows(q, "q", hq, d)
-    store = _describe(code, dev, page_table, lens, cu, n_pages, heads, page, d, 8, None, None,
-                      k_mean.data_ptr())
+    n, hq, _ = q.shape
+    qs = _rows(q, "q", n, hq, d)
+    store = _describe(code, dev, page_table, lens, cu, n_pages, heads, page, d, 8, None, None, mean)
     if out is None:
-        out = _new((n, heads, select), torch.int32, dev, stream)
+        out = _new((n, heads, select), _I32, dev, stream)
     else:
         _index(out, "out", 3, dev)
         if out.shape != (n, heads, select):
             raise ValueError(f"out must be [{n}, {heads}, {select}]")
-    lib = _lib()
-    need = lib.fastnn_select_workspace_size(store, n)
+    need = (_bound or _lib()).fastnn_select_workspace_size(store, n, hq, max_new)
     ws = _scratch(need, dev, workspace, "fastnn_select_workspace_size", stream)
-    with _On(dev, stream) as st:
-        rc = lib.fastnn_select_pages(store, q.data_ptr(), qs, n, hq, max_new, int(causal),
-                                     keep_first, keep_last, select, out.data_ptr(), ws.data_ptr(),
-                                     need, st)
-    _check(rc, "fastnn_select_pages")
+    _launch("fastnn_select_pages", dev, stream, store, q.data_ptr(), qs, n, hq, max_new, causal,
+            keep_first, keep_last, select, out.data_ptr(), ws.data_ptr(), need)
     return out

@@ -27,6 +27,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16;    // query rows of a block (one mma tile)
 constexpr int kUnit = 16;    // positions of a unit: the smallest page
 constexpr int kStages = 3;   // units in a warp's ring
+constexpr float kMostSum = 256.f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -96,8 +97,9 @@ struct RowsSmem {
 };
 
 // DP: head width padded to 32, 64 or 128. SEL: the positions are those of
-// a.pages' entries for the block's (single) token.
-template <typename T, int DP, bool SEL>
+// a.pages' entries for the block's (single) token. FULL: d == dv == DP, so a
+// unit's K and V are 16 * DP consecutive elements each.
+template <typename T, int DP, bool SEL, bool FULL>
 __global__ void __launch_bounds__(kThreads)
 attend_rows_kernel(AttendArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -155,7 +157,7 @@ attend_rows_kernel(AttendArgs a) {
     const int rr = r0 + (real ? r : 0);
     const int tok = SEL ? tok_first : rr / a.group;
     const int hd = g * a.group + (SEL ? rr : rr - tok * a.group);
-    vis[half] = real ? visible(w, tok) : 0;
+    vis[half] = real ? visible(w, tok) : vmax;  // a row that is not there has zero queries
     const uint16_t* qr = a.q + (static_cast<int64_t>(w.t0) + tok) * a.q_stride +
                          static_cast<int64_t>(hd) * st.d;
 #pragma unroll
@@ -199,9 +201,14 @@ attend_rows_kernel(AttendArgs a) {
     if constexpr (SEL) return lp * st.page + (u % upp) * kUnit;
     return k0 + u * kUnit;
   };
+  // Copies of one unit, 16 bytes a lane and step: step i takes chunk c of row
+  // row0 + i * kRowStep.
+  constexpr int kChunks = DP / 8, kSteps = kUnit * kChunks / 32, kRowStep = 32 / kChunks;
+  const int row0 = lane / kChunks, c0 = lane % kChunks;
+  const int64_t k_page = static_cast<int64_t>(st.page) * st.d, v_page = static_cast<int64_t>(st.page) * st.dv;
   // Positions of the ring's stages (-1: nothing there), as the warp knows them.
   int pos_ring[kStages];
-  auto issue = [&](int j) {
+  auto issue = [&](int j, int stage) {
     int pos = -1;
     if (j < mine) {
       if ((j & 31) == 0) fetch_ids(j);
@@ -210,19 +217,29 @@ attend_rows_kernel(AttendArgs a) {
       if (id >= 0) pos = unit_pos(j, lp);
       if (pos >= vmax) pos = -1;
       if (pos >= 0) {
-        const int64_t row =
-            (static_cast<int64_t>(id) * st.heads + g) * st.page + (pos & (st.page - 1));
-        const uint16_t* kp = st.k + row * st.d;
-        const uint16_t* vp = st.v + row * st.dv;
-        const uint32_t kd = ring + (j % kStages) * S::kStage, vd = kd + S::kTile;
-        constexpr int kChunks = DP / 8;
+        const int64_t slab = static_cast<int64_t>(id) * st.heads + g;
+        const int in_page = pos & (st.page - 1);
+        const uint32_t kd = ring + stage * S::kStage, vd = kd + S::kTile;
+        if (FULL && pos + kUnit <= vmax) {
+          const int64_t off = slab * k_page + in_page * DP + lane * 8;
+          const uint16_t* kp = st.k + off;
+          const uint16_t* vp = st.v + off;
 #pragma unroll
-        for (int i = 0; i < kUnit * kChunks / 32; ++i) {
-          const int c = (i * 32 + lane) % kChunks, r = (i * 32 + lane) / kChunks;
-          const bool there = pos + r < vmax;  // what lies behind the length is not read
-          const bool kr = there && c * 8 < st.d, vr = there && c * 8 < st.dv;
-          cp16(kd + chunk_at<DP>(r, c), kr ? kp + r * st.d + c * 8 : st.k, kr);
-          cp16(vd + chunk_at<DP>(r, c), vr ? vp + r * st.dv + c * 8 : st.v, vr);
+          for (int i = 0; i < kSteps; ++i) {
+            cp16(kd + chunk_at<DP>(row0 + i * kRowStep, c0), kp + i * 256, true);
+            cp16(vd + chunk_at<DP>(row0 + i * kRowStep, c0), vp + i * 256, true);
+          }
+        } else {
+          const uint16_t* kp = st.k + slab * k_page + in_page * st.d;
+          const uint16_t* vp = st.v + slab * v_page + in_page * st.dv;
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const int r = row0 + i * kRowStep;
+            const bool there = pos + r < vmax;  // what lies behind the length is not read
+            const bool kr = there && c0 * 8 < st.d, vr = there && c0 * 8 < st.dv;
+            cp16(kd + chunk_at<DP>(r, c0), kr ? kp + r * st.d + c0 * 8 : st.k, kr);
+            cp16(vd + chunk_at<DP>(r, c0), vr ? vp + r * st.dv + c0 * 8 : st.v, vr);
+          }
         }
       }
     }
@@ -232,8 +249,12 @@ attend_rows_kernel(AttendArgs a) {
 
   float o[DP / 8][4] = {};
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // Byte offsets of this lane's ldmatrix rows within a tile; the 16-column step
+  // ks of a row lies at this offset with ks * 32 exclusive-or'ed in.
+  const uint32_t k_off = chunk_at<DP>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+  const uint32_t v_off = chunk_at<DP>(lane & 15, lane >> 4);
 #pragma unroll
-  for (int j = 0; j < kStages - 1; ++j) pos_ring[j] = issue(j);
+  for (int j = 0; j < kStages - 1; ++j) pos_ring[j] = issue(j, j);
   for (int jb = 0; jb < mine; jb += kStages) {
 #pragma unroll
     for (int st_i = 0; st_i < kStages; ++st_i) {
@@ -243,69 +264,89 @@ attend_rows_kernel(AttendArgs a) {
       __syncwarp();
       const int pos = pos_ring[st_i];
       // The stage read at step j - 1 is free again: fill it before computing.
-      pos_ring[(st_i + kStages - 1) % kStages] = issue(j + kStages - 1);
+      constexpr int kBack = kStages - 1;
+      pos_ring[(st_i + kBack) % kStages] = issue(j + kBack, (st_i + kBack) % kStages);
       if (pos < 0) continue;
-      const uint32_t kd = ring + st_i * S::kStage, vd = kd + S::kTile;
+      const uint32_t kd = ring + st_i * S::kStage + k_off, vd = ring + st_i * S::kStage + S::kTile + v_off;
       float x[2][4] = {};
-      {
-        const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
 #pragma unroll
-        for (int ks = 0; ks < DP / 16; ++ks) {
-          uint32_t b[4];
-          ldsm4(kd + chunk_at<DP>(kr, ks * 2 + kc), b);
-          mma16816<T>(x[0], qa[ks], b[0], b[1]);
-          mma16816<T>(x[1], qa[ks], b[2], b[3]);
-        }
+      for (int ks = 0; ks < DP / 16; ++ks) {
+        uint32_t b[4];
+        ldsm4(kd ^ (ks * 32), b);
+        mma16816<T>(x[0], qa[ks], b[0], b[1]);
+        mma16816<T>(x[1], qa[ks], b[2], b[3]);
       }
+      // Weights by the maximum in force, each thread's share of their sums. The
+      // maximum need not be the largest score so far (O / l does not depend on
+      // it): it is sought, with the shuffles that takes, only when a thread's
+      // sum says that a weight may be far above 1.
       const bool edge = pos + kUnit > vmin;
-      float top[2] = {m[0], m[1]};
+      if (edge) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[t][e] *= a.scale_log2;
-          if (edge && pos + t * 8 + (lane & 3) * 2 + (e & 1) >= vis[e >> 1]) x[t][e] = -INFINITY;
-          top[e >> 1] = fmaxf(top[e >> 1], x[t][e]);
+          for (int e = 0; e < 4; ++e)
+            if (pos + t * 8 + (lane & 3) * 2 + (e & 1) >= vis[e >> 1]) x[t][e] = -INFINITY;
+      }
+      float y[2][4], sum[2];
+      auto weigh = [&]() {
+        const float z0 = m[0] == -INFINITY ? 0.f : -m[0], z1 = m[1] == -INFINITY ? 0.f : -m[1];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          y[t][0] = ex2(fmaf(x[t][0], a.scale_log2, z0));
+          y[t][1] = ex2(fmaf(x[t][1], a.scale_log2, z0));
+          y[t][2] = ex2(fmaf(x[t][2], a.scale_log2, z1));
+          y[t][3] = ex2(fmaf(x[t][3], a.scale_log2, z1));
         }
+        sum[0] = (y[0][0] + y[0][1]) + (y[1][0] + y[1][1]);
+        sum[1] = (y[0][2] + y[0][3]) + (y[1][2] + y[1][3]);
+      };
+      weigh();
+      if (__any_sync(0xffffffffu, sum[0] > kMostSum || sum[1] > kMostSum || m[0] == -INFINITY ||
+                                      m[1] == -INFINITY)) {
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 1));
-        top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 2));
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)  // a masked place stays out for a scale of any sign
+            if (x[t][e] != -INFINITY) top[e >> 1] = fmaxf(top[e >> 1], x[t][e] * a.scale_log2);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 1));
+          top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 2));
+          top[half] = fmaxf(top[half], m[half]);
+          // A row that has seen nothing yet has m = -inf: l and O are 0 then.
+          const float f = m[half] == top[half] ? 1.f : ex2(m[half] - top[half]);
+          l[half] *= f;
+          m[half] = top[half];
+#pragma unroll
+          for (int t = 0; t < DP / 8; ++t) {
+            o[t][2 * half] *= f;
+            o[t][2 * half + 1] *= f;
+          }
+        }
+        weigh();
       }
-      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
-        // A row that has seen nothing yet has m = -inf: l and O are 0 then.
-        const float f0 = m[0] == top[0] ? 1.f : ex2(m[0] - top[0]);
-        const float f1 = m[1] == top[1] ? 1.f : ex2(m[1] - top[1]);
-        l[0] *= f0;
-        l[1] *= f1;
-        m[0] = top[0];
-        m[1] = top[1];
+      if (edge) {  // and its weight is 0
 #pragma unroll
-        for (int t = 0; t < DP / 8; ++t) {
-          o[t][0] *= f0;
-          o[t][1] *= f0;
-          o[t][2] *= f1;
-          o[t][3] *= f1;
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (x[t][2 * half + e] == -INFINITY) y[t][2 * half + e] = 0.f;
+          sum[half] = (y[0][2 * half] + y[0][2 * half + 1]) + (y[1][2 * half] + y[1][2 * half + 1]);
         }
       }
-      const float z0 = m[0] == -INFINITY ? 0.f : m[0], z1 = m[1] == -INFINITY ? 0.f : m[1];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        x[t][0] = ex2(x[t][0] - z0);
-        x[t][1] = ex2(x[t][1] - z0);
-        x[t][2] = ex2(x[t][2] - z1);
-        x[t][3] = ex2(x[t][3] - z1);
-        l[0] += x[t][0] + x[t][1];
-        l[1] += x[t][2] + x[t][3];
-      }
+      l[0] += sum[0];
+      l[1] += sum[1];
       // The weights go to the tensor cores in the store's 16-bit type.
-      const uint32_t p[4] = {Half16<T>::pack(x[0][0], x[0][1]), Half16<T>::pack(x[0][2], x[0][3]),
-                             Half16<T>::pack(x[1][0], x[1][1]), Half16<T>::pack(x[1][2], x[1][3])};
-      const int vr = lane & 15, vc = lane >> 4;
+      const uint32_t p[4] = {Half16<T>::pack(y[0][0], y[0][1]), Half16<T>::pack(y[0][2], y[0][3]),
+                             Half16<T>::pack(y[1][0], y[1][1]), Half16<T>::pack(y[1][2], y[1][3])};
 #pragma unroll
       for (int t = 0; t < DP / 16; ++t) {
         uint32_t b[4];
-        ldsm4t(vd + chunk_at<DP>(vr, t * 2 + vc), b);
+        ldsm4t(vd ^ (t * 32), b);
         mma16816<T>(o[2 * t], p, b[0], b[1]);
         mma16816<T>(o[2 * t + 1], p, b[2], b[3]);
       }
@@ -393,6 +434,7 @@ attend_rows_kernel(AttendArgs a) {
 template <typename T, bool SEL>
 __global__ void __launch_bounds__(128)
 combine_kernel(AttendArgs a) {
+  cudaGridDependencySynchronize();
   const StoreArgs& st = a.st;
   const int s = blockIdx.y, lane = threadIdx.x & 31;
   const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
@@ -436,33 +478,39 @@ combine_kernel(AttendArgs a) {
     a.lse[row] = top > -INFINITY ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
-template <typename T, int DP, bool SEL>
+template <typename T, int DP, bool SEL, bool FULL>
 int rows_launch(const AttendArgs& a, cudaStream_t st) {
   using S = RowsSmem<DP>;
   static_assert(S::kTotal <= 227 * 1024, "shared memory of an SM");
-  FASTNN_CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<T, DP, SEL>,
+  FASTNN_CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<T, DP, SEL, FULL>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal));
   const int64_t tiles =
       SEL ? static_cast<int64_t>(a.max_new) * ((a.group + kRows - 1) / kRows)
           : (static_cast<int64_t>(a.max_new) * a.group + kRows - 1) / kRows;
   if (tiles * a.splits > INT32_MAX) return FASTNN_ERR_INVALID;
   const dim3 grid(static_cast<unsigned>(tiles * a.splits), a.st.heads, a.st.n_seqs);
-  attend_rows_kernel<T, DP, SEL><<<grid, kThreads, S::kTotal, st>>>(a);
+  attend_rows_kernel<T, DP, SEL, FULL><<<grid, kThreads, S::kTotal, st>>>(a);
   FASTNN_CUDA_TRY(cudaGetLastError());
   if (a.splits > 1) {
     const int64_t blocks = (static_cast<int64_t>(a.max_new) * a.hq + 3) / 4;
-    combine_kernel<T, SEL><<<dim3(static_cast<unsigned>(blocks), a.st.n_seqs), 128, 0, st>>>(a);
-    FASTNN_CUDA_TRY(cudaGetLastError());
+    FASTNN_CUDA_TRY(launch_after(combine_kernel<T, SEL>, dim3(static_cast<unsigned>(blocks), a.st.n_seqs),
+                                 dim3(128), st, a));
   }
   return FASTNN_OK;
+}
+
+template <typename T, int DP, bool SEL>
+int rows_full(const AttendArgs& a, cudaStream_t st) {
+  return a.st.d == DP && a.st.dv == DP ? rows_launch<T, DP, SEL, true>(a, st)
+                                       : rows_launch<T, DP, SEL, false>(a, st);
 }
 
 template <typename T, bool SEL>
 int rows_width(const AttendArgs& a, cudaStream_t st) {
   const int wide = a.st.d > a.st.dv ? a.st.d : a.st.dv;
-  if (wide <= 32) return rows_launch<T, 32, SEL>(a, st);
-  if (wide <= 64) return rows_launch<T, 64, SEL>(a, st);
-  return rows_launch<T, 128, SEL>(a, st);
+  if (wide <= 32) return rows_full<T, 32, SEL>(a, st);
+  if (wide <= 64) return rows_full<T, 64, SEL>(a, st);
+  return rows_full<T, 128, SEL>(a, st);
 }
 
 }  // namespace

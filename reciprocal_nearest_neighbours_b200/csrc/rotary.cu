@@ -143,7 +143,8 @@ rotary_kernel(const uint16_t* x, int64_t x_stride, int64_t n, int heads, int d, 
 }
 
 // One block writes the new rows of one page of one sequence and one head, and
-// then that page's mean. Block (0, 0, n_seqs) writes the status word.
+// then that page's mean. Block (0, 0, n_seqs), if there is one, writes the status
+// word.
 template <typename T, int V>
 __global__ void __launch_bounds__(kAppendThreads)
 append_kernel(StoreArgs st, const uint16_t* k, int64_t k_stride, const uint16_t* v,
@@ -293,7 +294,7 @@ int append_v(const StoreArgs& a, const uint16_t* k, int64_t k_stride, const uint
              cudaStream_t st) {
   const int touched = (max_new + a.page - 2) / a.page + 1;
   const size_t smem = r.rot ? kAppendRows * r.axes * r.nf * sizeof(float2) : 0;
-  append_kernel<T, V><<<dim3(touched, a.heads, a.n_seqs + 1), kAppendThreads, smem, st>>>(
+  append_kernel<T, V><<<dim3(touched, a.heads, a.n_seqs + (status != nullptr)), kAppendThreads, smem, st>>>(
       a, k, k_stride, v, v_stride, n, max_new, r, status);
   FASTNN_CUDA_TRY(cudaGetLastError());
   return FASTNN_OK;

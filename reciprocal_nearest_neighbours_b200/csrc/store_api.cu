@@ -153,9 +153,9 @@ int fastnn_store_append(const fastnn_store* store, const void* k, int64_t k_stri
   FASTNN_TRY(row_checks(v, v_stride, static_cast<int64_t>(store->heads) * store->dv));
   if (!store->k_pages || !aligned(store->k_pages, 16) || !store->v_pages ||
       !aligned(store->v_pages, 16) || !aligned(store->k_mean, 16) || !store->page_table ||
-      !store->lens || !store->cu || !workspace || !aligned(workspace, kAlign))
+      !store->lens || !store->cu || !aligned(workspace, kAlign))
     return FASTNN_ERR_INVALID;
-  if (workspace_bytes < FASTNN_STORE_APPEND_WORKSPACE) return FASTNN_ERR_CAPACITY;
+  if (workspace && workspace_bytes < FASTNN_STORE_APPEND_WORKSPACE) return FASTNN_ERR_CAPACITY;
   return launch_store_append(store_args(store), store->dtype, static_cast<const uint16_t*>(k),
                              k_stride, static_cast<const uint16_t*>(v), v_stride, n, max_new, r,
                              static_cast<int*>(workspace), reinterpret_cast<cudaStream_t>(stream));
@@ -199,8 +199,8 @@ int fastnn_attend(const fastnn_store* store, const void* q, int64_t q_stride, in
   return launch_attend_rows(a, store->dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t fastnn_select_workspace_size(const fastnn_store* store, int64_t n) {
-  if (store_sizes(store) != FASTNN_OK || n < 0) return 0;
+size_t fastnn_select_workspace_size(const fastnn_store* store, int64_t n, int heads_q, int max_new) {
+  if (attend_sizes(store, n, heads_q, max_new, 1) != FASTNN_OK) return 0;
   return kAlign;
 }
 
@@ -217,7 +217,7 @@ int fastnn_select_pages(const fastnn_store* store, const void* q, int64_t q_stri
   if (!store->k_mean || !aligned(store->k_mean, 16) || !store->page_table || !store->lens ||
       !store->cu || !out_pages || !aligned(out_pages, 4) || !workspace || !aligned(workspace, kAlign))
     return FASTNN_ERR_INVALID;
-  if (workspace_bytes < fastnn_select_workspace_size(store, n)) return FASTNN_ERR_CAPACITY;
+  if (workspace_bytes < fastnn_select_workspace_size(store, n, heads_q, max_new)) return FASTNN_ERR_CAPACITY;
   SelectArgs a{};
   a.st = store_args(store);
   a.q = static_cast<const uint16_t*>(q);

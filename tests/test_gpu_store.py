@@ -540,3 +540,46 @@ def test_pages_far_apart_in_a_large_store():
         st.k_pages[ph, 0, row], st.v_pages[ph, 0, row] = st.k[i, 0], st.v[i, 0]
     for h in (0, 7):
         ref.check_attend(out[:, h:h + 1], lse[:, h:h + 1], st)
+
+
+def test_refusals_of_shapes_types_and_devices():
+    z = lambda *s, dtype=BF16: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    kp, vp, table, lens, cu = z(4, 2, 16, 64), z(4, 2, 16, 64), i(2, 3), i(2), i(3)
+    q, freq = z(5, 4, 64), torch.zeros(4, dtype=torch.float64, device="cuda")
+    for args in ((q, kp.half(), vp, table, lens, cu), (q, kp, vp.half(), table, lens, cu)):
+        with pytest.raises(TypeError):
+            fnn.fastnn_attend(*args, 3)
+    for args in ((z(5, 3, 64), kp, vp, table, lens, cu), (q, kp, z(4, 2, 32, 64), table, lens, cu),
+                 (q, kp, vp, table.long(), lens, cu), (q, kp, vp, table, i(3), cu), (q, kp, vp, table, lens, i(4)),
+                 (q, kp, vp, table.cpu(), lens, cu), (q, kp.cpu(), vp, table, lens, cu),
+                 (z(5, 4, 128)[:, :, ::2], kp, vp, table, lens, cu),
+                 (z(5, 64, 4).transpose(1, 2), kp, vp, table, lens, cu),
+                 (q, kp[:, :, :, :32], vp, table, lens, cu), (q, kp, vp, table[:, ::2], lens, cu)):
+        with pytest.raises(ValueError):
+            fnn.fastnn_attend(*args, 3)
+    for kw in (dict(pages=i(5, 4, 2)), dict(pages=i(5, 2, 2).long()), dict(out=z(5, 4, 32)), dict(lse=z(5, 4)),
+               dict(out=z(5, 64, 4).transpose(1, 2)), dict(workspace=torch.zeros(4096, dtype=torch.uint8))):
+        with pytest.raises((ValueError, TypeError)):
+            fnn.fastnn_attend(q, kp, vp, table, lens, cu, 3, **kw)
+    for new in (0, 6):
+        with pytest.raises(fnn.FastNNError):
+            fnn.fastnn_attend(q, kp, vp, table, lens, cu, new)
+    with pytest.raises(fnn.FastNNError):  # a workspace too small
+        fnn.fastnn_attend(q, kp, vp, table, lens, cu, 3, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(fnn.FastNNError):  # rows at an address that is no multiple of 16 bytes
+        fnn.fastnn_attend(z(5 * 4 * 64 + 1)[1:].view(5, 4, 64), kp, vp, table, lens, cu, 3)
+    for kw in (dict(pos=i(4), freq=freq), dict(pos=i(5, 3), freq=freq), dict(pos=i(5), freq=freq.float()),
+               dict(pos=i(5), freq=freq, layout="quarter"), dict(pos=i(5).long(), freq=freq)):
+        with pytest.raises(ValueError):
+            fnn.fastnn_rotary(q, **kw)
+    with pytest.raises(ValueError):
+        fnn.fastnn_store_append(z(5, 2, 64), z(5, 2, 64), kp, vp, table, lens, cu, 3, pos=i(5))
+    with pytest.raises(ValueError):
+        fnn.fastnn_store_append(z(5, 2, 64), z(4, 2, 64), kp, vp, table, lens, cu, 3)
+    with pytest.raises(ValueError):
+        fnn.fastnn_store_append(z(5, 2, 64), z(5, 2, 64), kp, vp, table, lens, cu, 3, k_mean=z(4, 2, 32))
+    with pytest.raises(fnn.FastNNError):
+        fnn.fastnn_select_pages(q, z(4, 2, 64), table, lens, cu, 3, 16, 2, keep_first=2)
+    with pytest.raises(ValueError):
+        fnn.fastnn_select_pages(q, z(4, 3, 64), table, lens, cu, 3, 16, 2)

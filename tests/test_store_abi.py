@@ -21,16 +21,19 @@ def lib():
 
 
 def _desc(**kw):
+    """fastnn_store as the C compiler lays it out."""
     f = dict(k_pages=FAKE, v_pages=FAKE, k_mean=FAKE, page_table=FAKE, lens=FAKE, cu=FAKE, n_pages=9,
              n_seqs=2, table_width=4, page=16, heads=2, d=64, dv=64, dtype=fnn.FASTNN_BF16)
     f.update(kw)
-    return _store._Store(**f)
+    return _store._STORE.pack(*(f[k] or 0 for k in (
+        "k_pages", "v_pages", "k_mean", "page_table", "lens", "cu", "n_pages", "n_seqs", "table_width",
+        "page", "heads", "d", "dv", "dtype")))
 
 
 def _rot(**kw):
     f = dict(pos=FAKE, freq=FAKE, axes=1, rot=64, layout=0, scale=1.0)
     f.update(kw)
-    return _store._Rotation(**f)
+    return _store._ROTATION.pack(*(f[k] or 0 for k in ("pos", "freq", "axes", "rot", "layout", "scale")))
 
 
 STORE_FAULTS = [
@@ -45,15 +48,15 @@ STORE_FAULTS = [
 
 @pytest.mark.parametrize("change,status", STORE_FAULTS)
 def test_store_sizes_are_refused(lib, change, status):
-    s = _desc(**change)
+    s, heads = _desc(**change), max(1, change.get("heads", 2))
     big = 1 << 40
     assert lib.fastnn_store_append(s, FAKE, 8192, FAKE, 8192, 5, 3, None, FAKE, 256, None) == status
-    assert lib.fastnn_attend(s, FAKE, 8192, 5, 2 * max(1, s.heads), 3, 1, 1.0, None, 0, FAKE, FAKE, FAKE,
+    assert lib.fastnn_attend(s, FAKE, 8192, 5, 2 * heads, 3, 1, 1.0, None, 0, FAKE, FAKE, FAKE,
                              big, None) == status
-    assert lib.fastnn_select_pages(s, FAKE, 8192, 5, 2 * max(1, s.heads), 3, 1, 0, 1, 4, FAKE, FAKE, big,
+    assert lib.fastnn_select_pages(s, FAKE, 8192, 5, 2 * heads, 3, 1, 0, 1, 4, FAKE, FAKE, big,
                                    None) == status
-    assert lib.fastnn_attend_workspace_size(s, 5, 2 * max(1, s.heads), 3, 0) == 0
-    assert lib.fastnn_select_workspace_size(s, 5) == 0
+    assert lib.fastnn_attend_workspace_size(s, 5, 2 * heads, 3, 0) == 0
+    assert lib.fastnn_select_workspace_size(s, 5, 2 * heads, 3) == 0
 
 
 def test_append_refusals(lib):
@@ -64,7 +67,7 @@ def test_append_refusals(lib):
     assert call(n=-1) == -1 and call(n=1 << 31) == -1 and call(m=0) == -1 and call(m=6) == -1
     assert call(k=None) == -1 and call(v=None) == -1 and call(k=FAKE + 8) == -1 and call(v=FAKE + 2) == -1
     assert call(ks=120) == -1 and call(ks=132) == -1 and call(vs=64) == -1
-    assert call(ws=None) == -1 and call(ws=FAKE + 16) == -1 and call(nb=255) == -3
+    assert call(ws=FAKE + 16) == -1 and call(nb=255) == -3
     for name in ("k_pages", "v_pages", "page_table", "lens", "cu"):
         assert call(_desc(**{name: None})) == -1, name
     assert call(_desc(k_pages=FAKE + 8)) == -1 and call(_desc(k_mean=FAKE + 8)) == -1
@@ -127,32 +130,20 @@ def test_workspace_sizes(lib):
     assert fnn.fastnn_attend_workspace_size(5, 4, 2, 64, 64, 2, 3, 4, 16, dtype=torch.float32) == 0
 
 
-def test_python_checks():
+def test_tensors_must_be_16_bit_and_on_a_gpu():
     z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
     i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
-    kp, vp, table, lens, cu = z(4, 2, 16, 64), z(4, 2, 16, 64), i(2, 3), i(2), i(3)
-    q = z(5, 4, 64)
-    for bad in (dict(q=z(5, 4, 64, dtype=torch.float32)), dict(v=z(4, 2, 16, 64, dtype=torch.float16))):
-        with pytest.raises(TypeError):
-            fnn.fastnn_attend(bad.get("q", q), kp, bad.get("v", vp), table, lens, cu, 3)
-    for args in ((z(5, 3, 64), kp, vp, table, lens, cu), (q, kp, z(4, 2, 32, 64), table, lens, cu),
-                 (q, kp, vp, table.long(), lens, cu), (q, kp, vp, table, i(3), cu),
-                 (z(5, 4, 128)[:, :, ::2], kp, vp, table, lens, cu), (z(5, 64, 4).transpose(1, 2), kp, vp, table, lens, cu),
-                 (q, kp[:, :, :, :32], vp, table, lens, cu), (q, kp, vp, table, lens, cu)):
-        with pytest.raises(ValueError):  # the last one: not on a CUDA device
-            fnn.fastnn_attend(*args, 3)
-    with pytest.raises(ValueError):
-        fnn.fastnn_attend(q, kp, vp, table, lens, cu, 3, pages=i(5, 4, 2))
-    with pytest.raises(ValueError):
-        fnn.fastnn_rotary(q, i(4), torch.zeros(4, dtype=torch.float64))
-    with pytest.raises(ValueError):
-        fnn.fastnn_rotary(q, i(5), torch.zeros(4))
-    with pytest.raises(ValueError):
-        fnn.fastnn_rotary(q, i(5), torch.zeros(4, dtype=torch.float64), layout="quarter")
-    with pytest.raises(ValueError):
-        fnn.fastnn_store_append(z(5, 2, 64), z(5, 2, 64), kp, vp, table, lens, cu, 3, pos=i(5))
-    with pytest.raises(ValueError):
-        fnn.fastnn_store_append(z(5, 2, 64), z(4, 2, 64), kp, vp, table, lens, cu, 3)
+    store = z(4, 2, 16, 64), z(4, 2, 16, 64), i(2, 3), i(2), i(3)
+    freq = torch.zeros(4, dtype=torch.float64)
+    for dtype, error in ((torch.float32, TypeError), (torch.int8, TypeError), (torch.bfloat16, ValueError)):
+        with pytest.raises(error):
+            fnn.fastnn_attend(z(5, 4, 64, dtype=dtype), *store, 3)
+        with pytest.raises(error):
+            fnn.fastnn_rotary(z(5, 4, 64, dtype=dtype), i(5), freq)
+        with pytest.raises(error):
+            fnn.fastnn_store_append(z(5, 2, 64, dtype=dtype), z(5, 2, 64), *store, 3)
+        with pytest.raises(error):
+            fnn.fastnn_select_pages(z(5, 4, 64, dtype=dtype), z(4, 2, 64), *store[2:], 3, 16, 2)
     with pytest.raises(ValueError):
         fnn.fastnn_rotary_frequencies(10, axes=2)
 
