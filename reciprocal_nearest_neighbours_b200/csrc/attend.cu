@@ -2,17 +2,19 @@
 //
 //     out[t, h] = sum_p exp2(x_p - lse2) value[p],  x_p = scale * log2(e) * <q[t, h], key[p]>
 //
-// in one pass over the keys: a running maximum m, sum l and output O per row,
-//     m' = max(m, max x),  l' = l 2^(m - m') + sum 2^(x - m'),
-//     O' = O 2^(m - m') + 2^(x - m') V,
-// all in fp32. A block takes 16 rows of one sequence and key head (the rows are
-// (token, query head of the group), so a group's heads share the keys' read) and
-// one split of the positions. Its warps do not wait for one another: each
+// in one pass over the keys: a running reference m, sum l and output O per row,
+//     l' = l 2^(m - m') + sum 2^(x - m'),  O' = O 2^(m - m') + 2^(x - m') V,
+// all in fp32. A block takes 8 or 16 rows of one sequence and key head (the rows
+// are (token, query head of the group), so a group's heads share the keys' read)
+// and one split of the positions. Its warps do not wait for one another: each
 // streams every kWarps-th unit of 16 positions through its own cp.async ring,
 // keeps its own (m, l, O), and the warps merge once at the end. Splits leave
 // normalised partial outputs with their log2 sums, which combine_kernel weighs.
-// With few rows the work is bound by reading K and V once; the 16-row mma.sync
-// tile (m16n8k16) fits the few rows, and its rate is far from binding.
+// The products are mma.sync m16n8k16 with the KEYS as the 16 rows of the first
+// operand and the query rows as its 8 columns: S^T = K Q^T, O^T = V^T P^T. A group
+// of up to 8 heads then wastes no product, O takes half the registers that a
+// 16-row tile of queries would need, and 12 warps fit an SM. With few rows
+// the work is bound by reading K and V once.
 #include <type_traits>
 
 #include "store.cuh"
@@ -24,9 +26,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 16;    // query rows of a block (one mma tile)
 constexpr int kUnit = 16;    // positions of a unit: the smallest page
-constexpr int kStages = 3;   // units in a warp's ring
+constexpr int kStages = 2;   // units in a warp's ring
 constexpr float kMostSum = 256.f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -59,6 +60,14 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
+// Transposes an 8 x 8 matrix of 16-bit elements held by the warp (lane: row lane /
+// 4, elements 2 (lane % 4) and the next one).
+__device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -86,24 +95,28 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return static_cast<uint32_t>(r * DP * 2 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-template <int DP>
+// NT: groups of 8 query rows of a block.
+template <int DP, int NT>
 struct RowsSmem {
+  static constexpr int kRows = 8 * NT;
   static constexpr int kTile = kUnit * DP * 2;       // bytes of one K or V unit
   static constexpr int kStage = 2 * kTile;
   static constexpr int kRing = kStages * kStage;     // a warp's ring
   static constexpr int kMl = kWarps * kRing;         // then [kWarps][16] m and l
   static constexpr int kTotal = kMl + kWarps * kRows * 2 * 4;
-  static_assert(kRing >= kRows * DP * 4, "the merge reuses the ring");
+  static constexpr int kOutPitch = DP + 4;           // floats of a row in the merge
+  static_assert(kRing >= kRows * kOutPitch * 4, "the merge reuses the ring");
 };
 
 // DP: head width padded to 32, 64 or 128. SEL: the positions are those of
 // a.pages' entries for the block's (single) token. FULL: d == dv == DP, so a
 // unit's K and V are 16 * DP consecutive elements each.
-template <typename T, int DP, bool SEL, bool FULL>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int DP, int NT, bool SEL, bool FULL>
+__global__ void __launch_bounds__(kThreads, 3)
 attend_rows_kernel(AttendArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
-  using S = RowsSmem<DP>;
+  using S = RowsSmem<DP, NT>;
+  constexpr int kRows = S::kRows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int s = blockIdx.z, g = blockIdx.y;
   const int split = static_cast<int>(blockIdx.x) % a.splits;
@@ -147,17 +160,17 @@ attend_rows_kernel(AttendArgs a) {
     u_count = (k1 - k0 + kUnit - 1) / kUnit;
   }
 
-  // Query fragments (rows lane / 4 and + 8), zero beyond d and beyond nrows.
-  uint32_t qa[DP / 16][4];
-  int vis[2];
+  // Query fragments: row lane / 4 of each group of 8, zero beyond d and beyond
+  // nrows. The scores of a thread belong to rows 2 (lane % 4) and the next one.
+  uint32_t qb[DP / 16][NT][2];
+  int vis[NT][2];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = (lane >> 2) + 8 * half;
+  for (int n = 0; n < NT; ++n) {
+    const int r = (lane >> 2) + 8 * n;
     const bool real = r < nrows;
     const int rr = r0 + (real ? r : 0);
     const int tok = SEL ? tok_first : rr / a.group;
     const int hd = g * a.group + (SEL ? rr : rr - tok * a.group);
-    vis[half] = real ? visible(w, tok) : vmax;  // a row that is not there has zero queries
     const uint16_t* qr = a.q + (static_cast<int64_t>(w.t0) + tok) * a.q_stride +
                          static_cast<int64_t>(hd) * st.d;
 #pragma unroll
@@ -165,12 +178,15 @@ attend_rows_kernel(AttendArgs a) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int col = ks * 16 + c * 8 + (lane & 3) * 2;
-        qa[ks][half + 2 * c] =
-            real && col < st.d ? __ldg(reinterpret_cast<const uint32_t*>(qr + col)) : 0u;
+        qb[ks][n][c] = real && col < st.d ? __ldg(reinterpret_cast<const uint32_t*>(qr + col)) : 0u;
       }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // a row that is not there has zero queries and masks nothing more
+      const int q = (lane & 3) * 2 + e + 8 * n;
+      vis[n][e] = SEL || q >= nrows ? vmax : visible(w, (r0 + q) / a.group);
+    }
   }
-  const int vmin_lane = vis[0] < vis[1] ? vis[0] : vis[1];
-  const int vmin = __reduce_min_sync(0xffffffffu, vmin_lane);
+  const int vmin = SEL ? vmax : visible(w, tok_first);
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * S::kRing;
   const int mine = u_count > warp ? (u_count - warp + kWarps - 1) / kWarps : 0;
@@ -247,12 +263,14 @@ attend_rows_kernel(AttendArgs a) {
     return pos;
   };
 
-  float o[DP / 8][4] = {};
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[DP / 16][NT][4] = {};  // dims lane / 4 and + 8 of each 16, rows as the scores'
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
   // Byte offsets of this lane's ldmatrix rows within a tile; the 16-column step
   // ks of a row lies at this offset with ks * 32 exclusive-or'ed in.
-  const uint32_t k_off = chunk_at<DP>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
-  const uint32_t v_off = chunk_at<DP>(lane & 15, lane >> 4);
+  const uint32_t k_off = chunk_at<DP>(lane & 15, lane >> 4);
+  const uint32_t v_off = chunk_at<DP>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
 #pragma unroll
   for (int j = 0; j < kStages - 1; ++j) pos_ring[j] = issue(j, j);
   for (int jb = 0; jb < mine; jb += kStages) {
@@ -268,87 +286,103 @@ attend_rows_kernel(AttendArgs a) {
       pos_ring[(st_i + kBack) % kStages] = issue(j + kBack, (st_i + kBack) % kStages);
       if (pos < 0) continue;
       const uint32_t kd = ring + st_i * S::kStage + k_off, vd = ring + st_i * S::kStage + S::kTile + v_off;
-      float x[2][4] = {};
+      // Scores: positions lane / 4 (x[n][0], x[n][1]) and + 8, two rows each. Even
+      // and odd steps add up apart: half as long a chain of dependent products.
+      float x[NT][4] = {}, x2[NT][4] = {};
 #pragma unroll
-      for (int ks = 0; ks < DP / 16; ++ks) {
-        uint32_t b[4];
-        ldsm4(kd ^ (ks * 32), b);
-        mma16816<T>(x[0], qa[ks], b[0], b[1]);
-        mma16816<T>(x[1], qa[ks], b[2], b[3]);
+      for (int ks = 0; ks < DP / 16; ks += 2) {
+        uint32_t k1[4], k2[4];
+        ldsm4(kd ^ (ks * 32), k1);
+        ldsm4(kd ^ (ks * 32 + 32), k2);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma16816<T>(x[n], k1, qb[ks][n][0], qb[ks][n][1]);
+          mma16816<T>(x2[n], k2, qb[ks + 1][n][0], qb[ks + 1][n][1]);
+        }
       }
-      // Weights by the maximum in force, each thread's share of their sums. The
-      // maximum need not be the largest score so far (O / l does not depend on
-      // it): it is sought, with the shuffles that takes, only when a thread's
-      // sum says that a weight may be far above 1.
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] += x2[n][e];
       const bool edge = pos + kUnit > vmin;
       if (edge) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (pos + t * 8 + (lane & 3) * 2 + (e & 1) >= vis[e >> 1]) x[t][e] = -INFINITY;
+            if (pos + (lane >> 2) + (e >> 1) * 8 >= vis[n][e & 1]) x[n][e] = -INFINITY;
       }
-      float y[2][4], sum[2];
+      // Weights by the reference in force, and each thread's share of their sums.
+      // The reference need not be the largest score so far (O / l does not depend
+      // on it): a maximum is sought, with the shuffles that takes, only when a
+      // thread's sum says that a weight may be far above 1.
+      float y[NT][4], sum[NT][2];
       auto weigh = [&]() {
-        const float z0 = m[0] == -INFINITY ? 0.f : -m[0], z1 = m[1] == -INFINITY ? 0.f : -m[1];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          y[t][0] = ex2(fmaf(x[t][0], a.scale_log2, z0));
-          y[t][1] = ex2(fmaf(x[t][1], a.scale_log2, z0));
-          y[t][2] = ex2(fmaf(x[t][2], a.scale_log2, z1));
-          y[t][3] = ex2(fmaf(x[t][3], a.scale_log2, z1));
-        }
-        sum[0] = (y[0][0] + y[0][1]) + (y[1][0] + y[1][1]);
-        sum[1] = (y[0][2] + y[0][3]) + (y[1][2] + y[1][3]);
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float z = m[n][e] == -INFINITY ? 0.f : -m[n][e];
+            y[n][e] = ex2(fmaf(x[n][e], a.scale_log2, z));
+            y[n][e + 2] = ex2(fmaf(x[n][e + 2], a.scale_log2, z));
+            sum[n][e] = y[n][e] + y[n][e + 2];
+          }
       };
       weigh();
-      if (__any_sync(0xffffffffu, sum[0] > kMostSum || sum[1] > kMostSum || m[0] == -INFINITY ||
-                                      m[1] == -INFINITY)) {
-        float top[2] = {-INFINITY, -INFINITY};
+      bool raise = false;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)  // a masked place stays out for a scale of any sign
-            if (x[t][e] != -INFINITY) top[e >> 1] = fmaxf(top[e >> 1], x[t][e] * a.scale_log2);
+        for (int e = 0; e < 2; ++e) raise = raise || sum[n][e] > kMostSum || m[n][e] == -INFINITY;
+      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 1));
-          top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 2));
-          top[half] = fmaxf(top[half], m[half]);
-          // A row that has seen nothing yet has m = -inf: l and O are 0 then.
-          const float f = m[half] == top[half] ? 1.f : ex2(m[half] - top[half]);
-          l[half] *= f;
-          m[half] = top[half];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int t = 0; t < DP / 8; ++t) {
-            o[t][2 * half] *= f;
-            o[t][2 * half + 1] *= f;
+          for (int e = 0; e < 2; ++e) {
+            float top = m[n][e];  // a masked place stays out for a scale of any sign
+            if (x[n][e] != -INFINITY) top = fmaxf(top, x[n][e] * a.scale_log2);
+            if (x[n][e + 2] != -INFINITY) top = fmaxf(top, x[n][e + 2] * a.scale_log2);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            // A row that has seen nothing yet has m = -inf: l and O are 0 then.
+            const float f = m[n][e] == top ? 1.f : ex2(m[n][e] - top);
+            l[n][e] *= f;
+            m[n][e] = top;
+#pragma unroll
+            for (int t = 0; t < DP / 16; ++t) {
+              o[t][n][e] *= f;
+              o[t][n][e + 2] *= f;
+            }
           }
-        }
         weigh();
       }
       if (edge) {  // and its weight is 0
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (x[t][2 * half + e] == -INFINITY) y[t][2 * half + e] = 0.f;
-          sum[half] = (y[0][2 * half] + y[0][2 * half + 1]) + (y[1][2 * half] + y[1][2 * half + 1]);
+          for (int e = 0; e < 4; ++e)
+            if (x[n][e] == -INFINITY) y[n][e] = 0.f;
+          sum[n][0] = y[n][0] + y[n][2];
+          sum[n][1] = y[n][1] + y[n][3];
         }
       }
-      l[0] += sum[0];
-      l[1] += sum[1];
-      // The weights go to the tensor cores in the store's 16-bit type.
-      const uint32_t p[4] = {Half16<T>::pack(y[0][0], y[0][1]), Half16<T>::pack(y[0][2], y[0][3]),
-                             Half16<T>::pack(y[1][0], y[1][1]), Half16<T>::pack(y[1][2], y[1][3])};
+      // The weights go to the tensor cores in the store's 16-bit type, turned
+      // from (position, row) to the (row, position) fragments of an operand.
+      uint32_t p[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        l[n][0] += sum[n][0];
+        l[n][1] += sum[n][1];
+        p[n][0] = turn8x8(Half16<T>::pack(y[n][0], y[n][1]));
+        p[n][1] = turn8x8(Half16<T>::pack(y[n][2], y[n][3]));
+      }
 #pragma unroll
       for (int t = 0; t < DP / 16; ++t) {
-        uint32_t b[4];
-        ldsm4t(vd ^ (t * 32), b);
-        mma16816<T>(o[2 * t], p, b[0], b[1]);
-        mma16816<T>(o[2 * t + 1], p, b[2], b[3]);
+        uint32_t v[4];
+        ldsm4t(vd ^ (t * 32), v);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816<T>(o[t][n], v, p[n][0], p[n][1]);
       }
     }
   }
@@ -356,29 +390,30 @@ attend_rows_kernel(AttendArgs a) {
   __syncwarp();
 
   // Merge the warps: each leaves its rows' O (over its own ring), m and l.
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-    l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-  }
   float* mine_o = reinterpret_cast<float*>(smem + warp * S::kRing);
   float* ml = reinterpret_cast<float*>(smem + S::kMl);
-  {
-    const int r = lane >> 2, c = (lane & 3) * 2;
 #pragma unroll
-    for (int t = 0; t < DP / 8; ++t) {
-      *reinterpret_cast<float2*>(mine_o + r * DP + t * 8 + c) = make_float2(o[t][0], o[t][1]);
-      *reinterpret_cast<float2*>(mine_o + (r + 8) * DP + t * 8 + c) = make_float2(o[t][2], o[t][3]);
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float sum = l[n][e];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const int q = n * 8 + (lane & 3) * 2 + e;
+      if (lane < 4) {
+        ml[(warp * kRows + q) * 2] = m[n][e];
+        ml[(warp * kRows + q) * 2 + 1] = sum;
+      }
+#pragma unroll
+      for (int t = 0; t < DP / 16; ++t) {
+        mine_o[q * S::kOutPitch + t * 16 + (lane >> 2)] = o[t][n][e];
+        mine_o[q * S::kOutPitch + t * 16 + (lane >> 2) + 8] = o[t][n][e + 2];
+      }
     }
-    if ((lane & 3) == 0) {
-      ml[(warp * kRows + r) * 2] = m[0];
-      ml[(warp * kRows + r) * 2 + 1] = l[0];
-      ml[(warp * kRows + r + 8) * 2] = m[1];
-      ml[(warp * kRows + r + 8) * 2 + 1] = l[1];
-    }
-  }
   __syncthreads();
-  const int r = tid >> 3;  // 8 threads a row
+  constexpr int kPerRow = kThreads / kRows;  // threads a row
+  const int r = tid / kPerRow;
   if (r >= nrows) return;
   float top = -INFINITY;
 #pragma unroll
@@ -398,12 +433,12 @@ attend_rows_kernel(AttendArgs a) {
   const int64_t row = (static_cast<int64_t>(w.t0) + tok) * a.hq + hd;
   const bool whole = SEL ? a.splits == 1 : visible(w, tok) <= a.split_len;
   if (whole && split > 0) return;
-  for (int c = (tid & 7) * 4; c < st.dv; c += 32) {
+  for (int c = (tid % kPerRow) * 4; c < st.dv; c += kPerRow * 4) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int q = 0; q < kWarps; ++q) {
       const float4 y = *reinterpret_cast<const float4*>(
-          reinterpret_cast<const float*>(smem + q * S::kRing) + r * DP + c);
+          reinterpret_cast<const float*>(smem + q * S::kRing) + r * S::kOutPitch + c);
       v.x += f[q] * y.x;
       v.y += f[q] * y.y;
       v.z += f[q] * y.z;
@@ -420,7 +455,7 @@ attend_rows_kernel(AttendArgs a) {
       *reinterpret_cast<float4*>(a.part + (split * a.n * a.hq + row) * st.dv + c) = v;
     }
   }
-  if ((tid & 7) == 0) {
+  if (tid % kPerRow == 0) {
     if (!whole) {
       a.part_lse[split * a.n * a.hq + row] = lse2;
     } else if (a.lse) {
@@ -478,18 +513,28 @@ combine_kernel(AttendArgs a) {
     a.lse[row] = top > -INFINITY ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
-template <typename T, int DP, bool SEL, bool FULL>
+// Groups of 8 query rows of a block: one if no block would have more rows.
+int row_groups(const AttendArgs& a) {
+  const int64_t rows = a.pages ? a.group : static_cast<int64_t>(a.max_new) * a.group;
+  return rows <= 8 ? 1 : 2;
+}
+// Row tiles of a sequence and key head.
+int64_t row_tiles(const AttendArgs& a) {
+  const int per = 8 * row_groups(a);
+  return a.pages ? static_cast<int64_t>(a.max_new) * ((a.group + per - 1) / per)
+                 : (static_cast<int64_t>(a.max_new) * a.group + per - 1) / per;
+}
+
+template <typename T, int DP, int NT, bool SEL, bool FULL>
 int rows_launch(const AttendArgs& a, cudaStream_t st) {
-  using S = RowsSmem<DP>;
-  static_assert(S::kTotal <= 227 * 1024, "shared memory of an SM");
-  FASTNN_CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<T, DP, SEL, FULL>,
+  using S = RowsSmem<DP, NT>;
+  static_assert(3 * (S::kTotal + 1024) <= 228 * 1024, "three blocks fit an SM");
+  FASTNN_CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<T, DP, NT, SEL, FULL>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal));
-  const int64_t tiles =
-      SEL ? static_cast<int64_t>(a.max_new) * ((a.group + kRows - 1) / kRows)
-          : (static_cast<int64_t>(a.max_new) * a.group + kRows - 1) / kRows;
+  const int64_t tiles = row_tiles(a);
   if (tiles * a.splits > INT32_MAX) return FASTNN_ERR_INVALID;
   const dim3 grid(static_cast<unsigned>(tiles * a.splits), a.st.heads, a.st.n_seqs);
-  attend_rows_kernel<T, DP, SEL, FULL><<<grid, kThreads, S::kTotal, st>>>(a);
+  attend_rows_kernel<T, DP, NT, SEL, FULL><<<grid, kThreads, S::kTotal, st>>>(a);
   FASTNN_CUDA_TRY(cudaGetLastError());
   if (a.splits > 1) {
     const int64_t blocks = (static_cast<int64_t>(a.max_new) * a.hq + 3) / 4;
@@ -501,8 +546,10 @@ int rows_launch(const AttendArgs& a, cudaStream_t st) {
 
 template <typename T, int DP, bool SEL>
 int rows_full(const AttendArgs& a, cudaStream_t st) {
-  return a.st.d == DP && a.st.dv == DP ? rows_launch<T, DP, SEL, true>(a, st)
-                                       : rows_launch<T, DP, SEL, false>(a, st);
+  const bool full = a.st.d == DP && a.st.dv == DP;
+  if (row_groups(a) == 1)
+    return full ? rows_launch<T, DP, 1, SEL, true>(a, st) : rows_launch<T, DP, 1, SEL, false>(a, st);
+  return full ? rows_launch<T, DP, 2, SEL, true>(a, st) : rows_launch<T, DP, 2, SEL, false>(a, st);
 }
 
 template <typename T, bool SEL>
@@ -521,9 +568,7 @@ int rows_width(const AttendArgs& a, cudaStream_t st) {
 // selection) long, and splits beyond a row's length cost an empty block each.
 void attend_plan(AttendArgs& a) {
   const bool sel = a.pages != nullptr;
-  const int64_t rows = static_cast<int64_t>(a.max_new) * a.group;
-  const int64_t tiles = sel ? static_cast<int64_t>(a.max_new) * ((a.group + kRows - 1) / kRows)
-                            : (rows + kRows - 1) / kRows;
+  const int64_t tiles = row_tiles(a);
   const int64_t base = tiles * a.st.heads * a.st.n_seqs;
   const int64_t want = 4 * 2 * 148;
   int64_t splits = base >= want ? 1 : (want + base - 1) / base;
