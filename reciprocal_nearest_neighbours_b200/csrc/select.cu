@@ -6,12 +6,16 @@
 // The choice among nearly equal scores has to be the definition's, not the
 // summation order's, so scores are formed in fp64: the sum of the group's
 // queries is exact or nearly so, the products are, and the sums agree to about
-// 1e-16 whatever their order. A block takes up to kTok tokens of one sequence and key
-// head; a thread scores one page for all of them, so that a mean is read and
-// widened once for the block's tokens. The scores become order-preserving
-// 64-bit keys in shared memory (0: not a candidate, all ones: taken whatever
-// its score), and a warp per token finds the select-th largest key bit by bit
-// and writes the pages in ascending order.
+// 1e-16 whatever their order. A score kernel writes order-preserving 64-bit
+// keys (0: not a candidate, all ones: taken whatever its score):
+//   steps (fewer than kTile tokens a sequence): half a warp a page, 16 bytes a
+//       lane; bound by reading the means once, spread over all SMs;
+//   chunks: tiles of 64 tokens x 64 pages, 4 x 4 a thread, both operands widened
+//       to fp64 once a tile in shared memory; bound by the fp64 units.
+// A pick kernel then holds a row's keys in registers, finds the select-th
+// largest bit by bit (from the highest bit in which the row's keys differ), and
+// writes the pages in ascending order. The keys of a slab of tokens stay below
+// kSlabBytes, about half of L2.
 #include "store.cuh"
 
 namespace fastnn {
@@ -19,8 +23,10 @@ namespace fastnn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTok = 8;
-constexpr int kSmemKeys = 196608;  // bytes of keys a block may hold
+constexpr int kTile = 64;      // tokens, pages of a score tile
+constexpr int kDepth = 32;     // elements of d in shared memory at a time
+constexpr int kStepTokens = 8; // fewer new tokens a sequence: the step kernel
+constexpr int64_t kSlabBytes = 64 << 20;
 
 __device__ __forceinline__ uint64_t key_of(double x) {
   if (x != x) return 1;  // NaN: behind every number
@@ -30,82 +36,270 @@ __device__ __forceinline__ uint64_t key_of(double x) {
   return k < 2 ? 2 : k == ~0ull ? k - 1 : k;
 }
 
+__device__ __forceinline__ int seen_pages(const SelectArgs& a, const SeqView& w, int i) {
+  return (visible(w, i) + a.st.page - 1) >> a.st.page_log2;
+}
+
+// The key row of token i (of the slab) of sequence s and key head g.
+__device__ __forceinline__ uint64_t* key_row(const SelectArgs& a, int s, int i, int g) {
+  return a.keys + ((static_cast<int64_t>(s) * a.slab + i) * a.st.heads + g) * a.st.width;
+}
+
+__device__ __forceinline__ uint64_t candidate(const SelectArgs& a, int p, int seen, bool there, double x) {
+  if (!there) return 0;
+  return p < a.keep_first || p >= seen - a.keep_last ? ~0ull : key_of(x);
+}
+
+__device__ __forceinline__ int page_of(const SelectArgs& a, int s, int p) {
+  const int id = __ldg(a.st.table + static_cast<int64_t>(s) * a.st.width + p);
+  return id < a.st.n_pages ? id : -1;
+}
+
+// Block: 64 pages of one sequence and key head; a warp takes 8 of them, half a
+// warp one, lane l % 16 elements 8 (l % 16) and on.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-select_kernel(SelectArgs a, int tok_per_block, int key_stride) {
-  extern __shared__ __align__(16) uint8_t smem[];
+score_step_kernel(SelectArgs a) {
+  __shared__ double qs[128];
   const StoreArgs& st = a.st;
-  const int s = blockIdx.z, g = blockIdx.y, tid = threadIdx.x;
+  const int s = blockIdx.z, g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
-  const int i0 = static_cast<int>(blockIdx.x) * tok_per_block;
-  if (i0 >= w.n) return;
-  const int m = w.n - i0 < tok_per_block ? w.n - i0 : tok_per_block;
-  double* qs = reinterpret_cast<double*>(smem);                    // [d][kTok]
-  uint64_t* keys = reinterpret_cast<uint64_t*>(qs + st.d * kTok);  // [tok_per_block][key_stride]
-
-  for (int i = tid; i < st.d * kTok; i += kThreads) {
-    const int t = i / st.d, e = i - t * st.d;
-    double sum = 0.0;
-    if (t < m) {
-      const uint16_t* q = a.q + (static_cast<int64_t>(w.t0) + i0 + t) * a.q_stride +
-                          static_cast<int64_t>(g) * a.group * st.d + e;
-      for (int h = 0; h < a.group; ++h) sum += static_cast<double>(Half16<T>::one(__ldg(q + h * st.d)));
-    }
-    qs[e * kTok + t] = sum;
+  const int n = w.n - a.first < a.slab ? w.n - a.first : a.slab;
+  if (n <= 0) return;
+  const int p0 = blockIdx.x * 64 + warp * 8 + (lane >> 4);
+  const int last = seen_pages(a, w, a.first + n - 1);
+  if (static_cast<int>(blockIdx.x) * 64 >= last) return;
+  const int e0 = (lane & 15) * 8;
+  uint4 mean[4];
+  bool there[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int p = p0 + 2 * k;
+    const int id = p < last ? page_of(a, s, p) : -1;
+    there[k] = id >= 0;
+    mean[k] = make_uint4(0, 0, 0, 0);
+    if (there[k] && e0 < st.d)
+      mean[k] = __ldg(reinterpret_cast<const uint4*>(st.mean + (static_cast<int64_t>(id) * st.heads + g) * st.d + e0));
   }
-  __syncthreads();
-  const int vlast = visible(w, i0 + m - 1);
-  const int pages = (vlast + st.page - 1) >> st.page_log2;  // of the block's last token
-  for (int p = tid; p < pages; p += kThreads) {
-    const int id = __ldg(st.table + static_cast<int64_t>(s) * st.width + p);
-    const bool there = id >= 0 && id < st.n_pages;
-    double acc[kTok] = {};
-    if (there) {
-      const uint4* row = reinterpret_cast<const uint4*>(
-          st.mean + (static_cast<int64_t>(id) * st.heads + g) * st.d);
-      for (int c = 0; c < st.d / 8; ++c) {
-        const uint4 x = __ldg(row + c);
+  for (int i = 0; i < n; ++i) {
+    __syncthreads();
+    if (tid < 128) {
+      double sum = 0.0;
+      if (tid < st.d) {
+        const uint16_t* q = a.q + (static_cast<int64_t>(w.t0) + a.first + i) * a.q_stride +
+                            static_cast<int64_t>(g) * a.group * st.d + tid;
+        for (int h = 0; h < a.group; ++h) sum += static_cast<double>(Half16<T>::one(__ldg(q + h * st.d)));
+      }
+      qs[tid] = sum;
+    }
+    __syncthreads();
+    const int seen = seen_pages(a, w, a.first + i);
+    uint64_t* keys = key_row(a, s, i, g);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t xs[4] = {mean[k].x, mean[k].y, mean[k].z, mean[k].w};
+      double acc = 0.0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = Half16<T>::unpack(xs[e]);
+        acc += static_cast<double>(f.x) * qs[e0 + 2 * e];
+        acc += static_cast<double>(f.y) * qs[e0 + 2 * e + 1];
+      }
+#pragma unroll
+      for (int o = 8; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      const int p = p0 + 2 * k;
+      if ((lane & 15) == 0 && p < seen) keys[p] = candidate(a, p, seen, there[k], acc);
+    }
+  }
+}
+
+// Block: 64 tokens x 64 pages of one sequence and key head.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+score_chunk_kernel(SelectArgs a) {
+  __shared__ __align__(16) double qs[kDepth][kTile + 2], ms[kDepth][kTile + 2];
+  __shared__ int ids[kTile];
+  const StoreArgs& st = a.st;
+  const int tiles = (a.slab + kTile - 1) / kTile;
+  const int s = blockIdx.z / tiles, i0 = (blockIdx.z - s * tiles) * kTile, g = blockIdx.y, tid = threadIdx.x;
+  const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
+  const int n = (w.n - a.first < a.slab ? w.n - a.first : a.slab) - i0;
+  if (n <= 0) return;
+  const int m = n < kTile ? n : kTile;
+  const int pb = blockIdx.x * kTile;
+  const int last = seen_pages(a, w, a.first + i0 + m - 1);
+  if (pb >= last) return;
+  if (tid < kTile) ids[tid] = pb + tid < last ? page_of(a, s, pb + tid) : -1;
+  double acc[4][4] = {};
+  const int tx = (tid & 15) * 4, ty = (tid >> 4) * 4;  // pages, tokens
+  const uint16_t* q0 = a.q + (static_cast<int64_t>(w.t0) + a.first + i0) * a.q_stride +
+                       static_cast<int64_t>(g) * a.group * st.d;
+  for (int e0 = 0; e0 < st.d; e0 += kDepth) {
+    __syncthreads();
+    // A thread fills 8 elements of one token and of one page.
+    const int row = tid >> 2, e = (tid & 3) * 8;
+    double sum[8] = {};
+    if (row < m && e0 + e < st.d)
+      for (int h = 0; h < a.group; ++h) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(q0 + row * a.q_stride + h * st.d + e0 + e));
         const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = Half16<T>::unpack(xs[i]);
-          const double lo = f.x, hi = f.y;
-          const double* q = qs + (c * 8 + 2 * i) * kTok;
-#pragma unroll
-          for (int t = 0; t < kTok; ++t) acc[t] += lo * q[t];
-#pragma unroll
-          for (int t = 0; t < kTok; ++t) acc[t] += hi * q[kTok + t];
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = Half16<T>::unpack(xs[k]);
+          sum[2 * k] += static_cast<double>(f.x);
+          sum[2 * k + 1] += static_cast<double>(f.y);
         }
+      }
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (ids[row] >= 0 && e0 + e < st.d)
+      x = __ldg(reinterpret_cast<const uint4*>(
+          st.mean + (static_cast<int64_t>(ids[row]) * st.heads + g) * st.d + e0 + e));
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = Half16<T>::unpack(xs[k]);
+      qs[e + 2 * k][row] = sum[2 * k];
+      qs[e + 2 * k + 1][row] = sum[2 * k + 1];
+      ms[e + 2 * k][row] = f.x;
+      ms[e + 2 * k + 1][row] = f.y;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int k = 0; k < kDepth; ++k) {
+      const double2 q01 = *reinterpret_cast<const double2*>(&qs[k][ty]);
+      const double2 q23 = *reinterpret_cast<const double2*>(&qs[k][ty + 2]);
+      const double2 m01 = *reinterpret_cast<const double2*>(&ms[k][tx]);
+      const double2 m23 = *reinterpret_cast<const double2*>(&ms[k][tx + 2]);
+      const double q[4] = {q01.x, q01.y, q23.x, q23.y}, p[4] = {m01.x, m01.y, m23.x, m23.y};
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[t][c] += q[t] * p[c];
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    if (ty + t >= m) break;
+    const int seen = seen_pages(a, w, a.first + i0 + ty + t);
+    uint64_t* keys = key_row(a, s, i0 + ty + t, g);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int p = pb + tx + c;
+      if (p < seen) keys[p] = candidate(a, p, seen, ids[tx + c] >= 0, acc[t][c]);
+    }
+  }
+}
+
+// W warps a row. Thread r of the row holds keys [r * K, r * K + K) in registers
+// (K == 0: any number, read again and again).
+template <int W, int K>
+__global__ void __launch_bounds__(kThreads)
+pick_kernel(SelectArgs a) {
+  cudaGridDependencySynchronize();
+  constexpr int kRow = 32 * W;
+  __shared__ int parts[2][8];
+  __shared__ uint64_t ends[2][8];
+  const StoreArgs& st = a.st;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = W == 1 ? lane : tid;
+  const int64_t row = W == 1 ? static_cast<int64_t>(blockIdx.x) * 8 + warp : blockIdx.x;
+  const int g = static_cast<int>(row % st.heads);
+  const int64_t si = row / st.heads;
+  const int s = static_cast<int>(si / a.slab), i = static_cast<int>(si - static_cast<int64_t>(s) * a.slab);
+  if (s >= st.n_seqs) return;
+  const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
+  if (a.first + i >= w.n) return;
+  const int seen = seen_pages(a, w, a.first + i);
+  const uint64_t* keys = key_row(a, s, i, g);
+  const int per = K ? K : (seen + kRow - 1) / kRow;
+  const int p0 = r * per;
+  uint64_t held[K ? K : 1];
+  if (K) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) held[k] = p0 + k < seen ? keys[p0 + k] : 0;
+  }
+  auto key = [&](int k) -> uint64_t {
+    if (K) return held[k];
+    return p0 + k < seen ? keys[p0 + k] : 0;
+  };
+  int turn = 0;
+  auto total = [&](int c) {  // over the row
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (W > 1) {
+      if (lane == 0) parts[turn][warp] = c;
+      __syncthreads();
+      c = 0;
+#pragma unroll
+      for (int q = 0; q < W; ++q) c += parts[turn][q];
+      turn ^= 1;
+    }
+    return c;
+  };
+  auto before = [&](int c) {  // over the threads of the row before this one
+    int x = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int all = __shfl_sync(0xffffffffu, x, 31);
+    x -= c;
+    if (W > 1) {
+      if (lane == 0) parts[turn][warp] = all;
+      __syncthreads();
+      for (int q = 0; q < warp; ++q) x += parts[turn][q];
+      turn ^= 1;
+    }
+    return x;
+  };
+  auto count = [&](uint64_t level) {
+    int c = 0;
+    if (K) {
+#pragma unroll
+      for (int k = 0; k < (K ? K : 1); ++k) c += held[k] >= level;
+    } else {
+      for (int k = 0; k < per; ++k) c += key(k) >= level;
+    }
+    return total(c);
+  };
+  // The largest level that at least `select` keys reach (1: every candidate is
+  // taken), and how many of the keys equal to it are (room < 0: all).
+  uint64_t level = 1;
+  int room = -1;
+  if (count(1) > a.select) {
+    // Bits above the highest one in which the candidates differ are common.
+    uint64_t lo = ~0ull, hi = 0;
+    for (int k = 0; k < per; ++k) {
+      const uint64_t x = K ? held[K ? k : 0] : key(k);
+      if (x) {
+        lo = x < lo ? x : lo;
+        hi = x > hi ? x : hi;
       }
     }
 #pragma unroll
-    for (int t = 0; t < kTok; ++t) {
-      if (t >= m) break;
-      const int seen = (visible(w, i0 + t) + st.page - 1) >> st.page_log2;
-      uint64_t key = 0;
-      if (there && p < seen)
-        key = p < a.keep_first || p >= seen - a.keep_last ? ~0ull : key_of(acc[t]);
-      keys[t * key_stride + p] = key;
+    for (int o = 16; o; o >>= 1) {
+      const uint64_t l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
+      lo = l2 < lo ? l2 : lo;
+      hi = h2 > hi ? h2 : hi;
     }
-  }
-  __syncthreads();
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int t = warp; t < m; t += kThreads / 32) {
-    const uint64_t* k = keys + t * key_stride;
-    const int seen = (visible(w, i0 + t) + st.page - 1) >> st.page_log2;
-    auto count = [&](uint64_t level) {
-      int c = 0;
-      for (int p = lane; p < seen; p += 32) c += k[p] >= level;
-      return __reduce_add_sync(0xffffffffu, c);
-    };
-    // The largest level that at least `select` keys reach (or 1: every
-    // candidate is taken), and how many of the keys equal to it are.
-    uint64_t level = 1;
-    int room = INT32_MAX;
-    if (count(1) > a.select) {
-      level = 0;
-      int reach = 0;
-      for (int b = 63; b >= 0; --b) {
+    if (W > 1) {
+      if (lane == 0) {
+        ends[0][warp] = lo;
+        ends[1][warp] = hi;
+      }
+      __syncthreads();
+      for (int q = 0; q < W; ++q) {
+        lo = ends[0][q] < lo ? ends[0][q] : lo;
+        hi = ends[1][q] > hi ? ends[1][q] : hi;
+      }
+    }
+    level = hi;
+    int reach = a.select;
+    if (lo != hi) {
+      const int top = 63 - __clzll(static_cast<long long>(lo ^ hi));
+      level = top == 63 ? 0 : (hi >> (top + 1)) << (top + 1);
+      reach = a.select + 1;  // more than select keys reach the common bits
+      for (int b = top; b >= 0; --b) {
         const uint64_t up = level | (1ull << b);
         const int c = count(up);
         if (c >= a.select) {
@@ -114,45 +308,86 @@ select_kernel(SelectArgs a, int tok_per_block, int key_stride) {
           if (c == a.select) break;
         }
       }
-      if (reach > a.select) room = a.select - (level == ~0ull ? 0 : count(level + 1));
+    } else {
+      reach = a.select + 1;
     }
-    int32_t* out = a.out + ((static_cast<int64_t>(w.t0) + i0 + t) * st.heads + g) * a.select;
-    int done = 0, ties = 0;
-    for (int p0 = 0; p0 < seen && done < a.select; p0 += 32) {
-      const uint64_t key = p0 + lane < seen ? k[p0 + lane] : 0;
-      const bool tie = room != INT32_MAX && key == level;
-      const unsigned tied = __ballot_sync(0xffffffffu, tie);
-      const int before = ties + __popc(tied & ((1u << lane) - 1u));
-      const bool take = key >= level && key > 0 && (!tie || before < room);
-      const unsigned taken = __ballot_sync(0xffffffffu, take);
-      const int at = done + __popc(taken & ((1u << lane) - 1u));
-      if (take && at < a.select) out[at] = p0 + lane;
-      ties += __popc(tied);
-      done += __popc(taken);
-    }
-    for (int i = done + lane; i < a.select; i += 32) out[i] = -1;
+    if (reach > a.select) room = a.select - (level == ~0ull ? 0 : count(level + 1));
   }
+  int ties = 0, more = 0;
+  if (room >= 0) {
+    for (int k = 0; k < per; ++k) ties += (K ? held[K ? k : 0] : key(k)) == level;
+    ties = before(ties);  // equal keys in the threads before
+  }
+  int t = ties;
+  for (int k = 0; k < per; ++k) {
+    const uint64_t x = K ? held[K ? k : 0] : key(k);
+    more += x > level || (x == level && (room < 0 || t < room));
+    t += x == level;
+  }
+  int at = before(more);
+  int32_t* out = a.out + ((static_cast<int64_t>(w.t0) + a.first + i) * st.heads + g) * a.select;
+  t = ties;
+  for (int k = 0; k < per; ++k) {
+    const uint64_t x = K ? held[K ? k : 0] : key(k);
+    const bool take = x > level || (x == level && (room < 0 || t < room));
+    t += x == level;
+    if (take && at < a.select) out[at++] = p0 + k;
+  }
+  const int taken = total(more);
+  for (int k = taken + r; k < a.select; k += kRow) out[k] = -1;
+}
+
+// Tokens of one slab: their keys stay below kSlabBytes (at least one tile).
+int64_t slab_tokens(const StoreArgs& st, int max_new) {
+  int64_t n = kSlabBytes / (static_cast<int64_t>(st.n_seqs) * st.heads * st.width * 8);
+  n = n / kTile * kTile;
+  if (n < kTile) n = kTile;
+  return n < max_new ? n : max_new;
+}
+
+template <int W, int K>
+cudaError_t pick(const SelectArgs& a, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(a.st.n_seqs) * a.slab * a.st.heads;
+  const int64_t blocks = W == 1 ? (rows + 7) / 8 : rows;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_after(pick_kernel<W, K>, dim3(static_cast<unsigned>(blocks)), dim3(W == 1 ? kThreads : 32 * W), st, a);
 }
 
 template <typename T>
-int select_t(const SelectArgs& a, cudaStream_t st) {
-  const int key_stride = a.st.width;
-  int tok = kSmemKeys / 8 / key_stride;
-  if (tok > kTok) tok = kTok;
-  if (tok > a.max_new) tok = a.max_new;
-  if (tok < 1) return FASTNN_ERR_UNSUPPORTED;
-  const size_t smem = static_cast<size_t>(a.st.d) * kTok * 8 + static_cast<size_t>(tok) * key_stride * 8;
-  FASTNN_CUDA_TRY(cudaFuncSetAttribute(select_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSmemKeys + 128 * kTok * 8));
-  const int blocks = (a.max_new + tok - 1) / tok;
-  select_kernel<T><<<dim3(blocks, a.st.heads, a.st.n_seqs), kThreads, smem, st>>>(a, tok, key_stride);
-  FASTNN_CUDA_TRY(cudaGetLastError());
+int select_t(const SelectArgs& all, cudaStream_t st) {
+  SelectArgs a = all;
+  a.slab = static_cast<int>(slab_tokens(a.st, a.max_new));
+  const int tiles = (a.slab + kTile - 1) / kTile;
+  const int page_blocks = (a.st.width + kTile - 1) / kTile;
+  const bool step = a.max_new < kStepTokens;
+  if (!step && static_cast<int64_t>(tiles) * a.st.n_seqs > 65535) {
+    // Too many tiles for one grid dimension: a tile of tokens at a time.
+    a.slab = kTile;
+  }
+  for (a.first = 0; a.first < a.max_new; a.first += a.slab) {
+    if (step) {
+      score_step_kernel<T><<<dim3(page_blocks, a.st.heads, a.st.n_seqs), kThreads, 0, st>>>(a);
+    } else {
+      const unsigned z = static_cast<unsigned>((a.slab + kTile - 1) / kTile) * a.st.n_seqs;
+      score_chunk_kernel<T><<<dim3(page_blocks, a.st.heads, z), kThreads, 0, st>>>(a);
+    }
+    FASTNN_CUDA_TRY(cudaGetLastError());
+    const int width = a.st.width;
+    FASTNN_CUDA_TRY(width <= 128    ? (pick<1, 4>(a, st))
+                    : width <= 256  ? (pick<1, 8>(a, st))
+                    : width <= 512  ? (pick<1, 16>(a, st))
+                    : width <= 1024 ? (pick<8, 4>(a, st))
+                    : width <= 4096 ? (pick<8, 16>(a, st))
+                                    : (pick<8, 0>(a, st)));
+  }
   return FASTNN_OK;
 }
 
 }  // namespace
 
-int select_max_width() { return kSmemKeys / 8; }
+size_t select_key_bytes(const StoreArgs& st, int max_new) {
+  return static_cast<size_t>(st.n_seqs) * slab_tokens(st, max_new) * st.heads * st.width * 8;
+}
 
 int launch_select(const SelectArgs& a, int dtype, cudaStream_t st) {
   return dtype == FASTNN_BF16 ? select_t<__nv_bfloat16>(a, st) : select_t<__half>(a, st);

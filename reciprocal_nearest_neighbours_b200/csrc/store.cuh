@@ -59,6 +59,8 @@ struct SelectArgs {
   int hq, group, max_new, causal;
   int keep_first, keep_last, select;
   int32_t* out;
+  uint64_t* keys;   // [n_seqs][slab][heads][width] of the slab's tokens
+  int slab, first;  // tokens of a slab; first token (of each sequence) of this one
 };
 
 // The new tokens of sequence s: first token, how many are taken, and the
@@ -153,7 +155,7 @@ bool attend_tc_takes(const AttendArgs& a);
 size_t attend_tc_floats(const AttendArgs& a);
 int launch_attend_tc(const AttendArgs& a, int dtype, cudaStream_t st);
 int launch_select(const SelectArgs& a, int dtype, cudaStream_t st);
-int select_max_width();
+size_t select_key_bytes(const StoreArgs& st, int max_new);
 uint64_t wait_timeout_ns();  // the limit set by fastnn_set_wait_timeout_ns (0: the default)
 
 }  // namespace fastnn

@@ -201,7 +201,7 @@ int fastnn_attend(const fastnn_store* store, const void* q, int64_t q_stride, in
 
 size_t fastnn_select_workspace_size(const fastnn_store* store, int64_t n, int heads_q, int max_new) {
   if (attend_sizes(store, n, heads_q, max_new, 1) != FASTNN_OK) return 0;
-  return kAlign;
+  return n == 0 ? kAlign : align_up(select_key_bytes(store_args(store), max_new));
 }
 
 int fastnn_select_pages(const fastnn_store* store, const void* q, int64_t q_stride, int64_t n,
@@ -209,7 +209,6 @@ int fastnn_select_pages(const fastnn_store* store, const void* q, int64_t q_stri
                         int select, int32_t* out_pages, void* workspace, size_t workspace_bytes,
                         fastnn_stream_t stream) {
   FASTNN_TRY(attend_sizes(store, n, heads_q, max_new, select));
-  if (store->table_width > select_max_width()) return FASTNN_ERR_UNSUPPORTED;
   if (keep_first < 0 || keep_last < 1 || select > 256 || keep_first > select - keep_last)
     return FASTNN_ERR_INVALID;
   if (n == 0) return FASTNN_OK;
@@ -231,6 +230,7 @@ int fastnn_select_pages(const fastnn_store* store, const void* q, int64_t q_stri
   a.keep_last = keep_last;
   a.select = select;
   a.out = out_pages;
+  a.keys = static_cast<uint64_t*>(workspace);
   return launch_select(a, store->dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
