@@ -10,8 +10,9 @@
 // keys (0: not a candidate, all ones: taken whatever its score):
 //   steps (fewer than kTile tokens a sequence): half a warp a page, 16 bytes a
 //       lane; bound by reading the means once, spread over all SMs;
-//   chunks: tiles of 64 tokens x 64 pages, 4 x 4 a thread, both operands widened
-//       to fp64 once a tile in shared memory; bound by the fp64 units.
+//   chunks: the groups' sums once by a kernel of their own, then tiles of 64
+//       tokens x 64 pages, 4 x 4 a thread, both operands as fp64 in shared memory;
+//       bound by the fp64 units and the shared memory that feeds them.
 // A pick kernel then holds a row's keys in registers, finds the select-th
 // largest bit by bit (from the highest bit in which the row's keys differ), and
 // writes the pages in ascending order. The keys of a slab of tokens stay below
@@ -113,11 +114,46 @@ score_step_kernel(SelectArgs a) {
   }
 }
 
+// The sums of the groups' queries in fp64, 8 elements a thread: every page tile
+// reads them, and widening is slow (a few elements a clock and SM).
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+sum_kernel(SelectArgs a) {
+  const StoreArgs& st = a.st;
+  const int s = blockIdx.y, per = st.heads * (st.d / 8);
+  const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
+  const int n = w.n - a.first < a.slab ? w.n - a.first : a.slab;
+  for (int64_t x = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+       x < static_cast<int64_t>(n) * per; x += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int i = static_cast<int>(x / per), c = static_cast<int>(x - static_cast<int64_t>(i) * per);
+    const int g = c / (st.d / 8), e = (c - g * (st.d / 8)) * 8;
+    const uint16_t* q = a.q + (static_cast<int64_t>(w.t0) + a.first + i) * a.q_stride +
+                        static_cast<int64_t>(g) * a.group * st.d + e;
+    double sum[8] = {};
+#pragma unroll 4
+    for (int h = 0; h < a.group; ++h) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(q + h * st.d));
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = Half16<T>::unpack(xs[k]);
+        sum[2 * k] += static_cast<double>(f.x);
+        sum[2 * k + 1] += static_cast<double>(f.y);
+      }
+    }
+    double2* out = reinterpret_cast<double2*>(
+        a.sums + ((static_cast<int64_t>(s) * a.slab + i) * st.heads + g) * st.d + e);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[k] = make_double2(sum[2 * k], sum[2 * k + 1]);
+  }
+}
+
 // Block: 64 tokens x 64 pages of one sequence and key head.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 score_chunk_kernel(SelectArgs a) {
-  __shared__ __align__(16) double qs[kDepth][kTile + 2], ms[kDepth][kTile + 2];
+  cudaGridDependencySynchronize();
+  __shared__ double qs[kDepth][kTile + 1], ms[kDepth][kTile + 1];
   __shared__ int ids[kTile];
   const StoreArgs& st = a.st;
   const int tiles = (a.slab + kTile - 1) / kTile;
@@ -130,47 +166,44 @@ score_chunk_kernel(SelectArgs a) {
   const int last = seen_pages(a, w, a.first + i0 + m - 1);
   if (pb >= last) return;
   if (tid < kTile) ids[tid] = pb + tid < last ? page_of(a, s, pb + tid) : -1;
+  __syncthreads();
+  // A thread fetches 8 elements of one token and of one page at a time, a step
+  // ahead of the products.
+  const int row = tid >> 2, e = (tid & 3) * 8;
+  const double* q0 = a.sums + ((static_cast<int64_t>(s) * a.slab + i0 + row) * st.heads + g) * st.d + e;
+  const uint16_t* m0 = st.mean + (static_cast<int64_t>(ids[row]) * st.heads + g) * st.d + e;
+  double2 qn[4];
+  uint4 mn;
+  auto fetch = [&](int e0) {
+    const bool in = e0 + e < st.d;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      qn[k] = in && row < m ? __ldcg(reinterpret_cast<const double2*>(q0 + e0) + k) : make_double2(0.0, 0.0);
+    mn = in && ids[row] >= 0 ? __ldg(reinterpret_cast<const uint4*>(m0 + e0)) : make_uint4(0, 0, 0, 0);
+  };
+  fetch(0);
   double acc[4][4] = {};
-  const int tx = (tid & 15) * 4, ty = (tid >> 4) * 4;  // pages, tokens
-  const uint16_t* q0 = a.q + (static_cast<int64_t>(w.t0) + a.first + i0) * a.q_stride +
-                       static_cast<int64_t>(g) * a.group * st.d;
+  const int tx = tid & 15, ty = (tid >> 4) * 4;  // pages tx + 16 c, tokens ty + t
   for (int e0 = 0; e0 < st.d; e0 += kDepth) {
     __syncthreads();
-    // A thread fills 8 elements of one token and of one page.
-    const int row = tid >> 2, e = (tid & 3) * 8;
-    double sum[8] = {};
-    if (row < m && e0 + e < st.d)
-      for (int h = 0; h < a.group; ++h) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(q0 + row * a.q_stride + h * st.d + e0 + e));
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = Half16<T>::unpack(xs[k]);
-          sum[2 * k] += static_cast<double>(f.x);
-          sum[2 * k + 1] += static_cast<double>(f.y);
-        }
-      }
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (ids[row] >= 0 && e0 + e < st.d)
-      x = __ldg(reinterpret_cast<const uint4*>(
-          st.mean + (static_cast<int64_t>(ids[row]) * st.heads + g) * st.d + e0 + e));
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+    const uint32_t xs[4] = {mn.x, mn.y, mn.z, mn.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 f = Half16<T>::unpack(xs[k]);
-      qs[e + 2 * k][row] = sum[2 * k];
-      qs[e + 2 * k + 1][row] = sum[2 * k + 1];
+      qs[e + 2 * k][row] = qn[k].x;
+      qs[e + 2 * k + 1][row] = qn[k].y;
       ms[e + 2 * k][row] = f.x;
       ms[e + 2 * k + 1][row] = f.y;
     }
     __syncthreads();
-#pragma unroll 4
+    if (e0 + kDepth < st.d) fetch(e0 + kDepth);
+#pragma unroll 8
     for (int k = 0; k < kDepth; ++k) {
-      const double2 q01 = *reinterpret_cast<const double2*>(&qs[k][ty]);
-      const double2 q23 = *reinterpret_cast<const double2*>(&qs[k][ty + 2]);
-      const double2 m01 = *reinterpret_cast<const double2*>(&ms[k][tx]);
-      const double2 m23 = *reinterpret_cast<const double2*>(&ms[k][tx + 2]);
-      const double q[4] = {q01.x, q01.y, q23.x, q23.y}, p[4] = {m01.x, m01.y, m23.x, m23.y};
+      double q[4], p[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) q[c] = qs[k][ty + c];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) p[c] = ms[k][tx + 16 * c];
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -184,8 +217,8 @@ score_chunk_kernel(SelectArgs a) {
     uint64_t* keys = key_row(a, s, i0 + ty + t, g);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int p = pb + tx + c;
-      if (p < seen) keys[p] = candidate(a, p, seen, ids[tx + c] >= 0, acc[t][c]);
+      const int p = pb + tx + 16 * c;
+      if (p < seen) keys[p] = candidate(a, p, seen, ids[tx + 16 * c] >= 0, acc[t][c]);
     }
   }
 }
@@ -367,11 +400,15 @@ int select_t(const SelectArgs& all, cudaStream_t st) {
   for (a.first = 0; a.first < a.max_new; a.first += a.slab) {
     if (step) {
       score_step_kernel<T><<<dim3(page_blocks, a.st.heads, a.st.n_seqs), kThreads, 0, st>>>(a);
+      FASTNN_CUDA_TRY(cudaGetLastError());
     } else {
+      const int64_t items = static_cast<int64_t>(a.slab) * a.st.heads * (a.st.d / 8);
+      const int64_t blocks = (items + kThreads - 1) / kThreads;
+      sum_kernel<T><<<dim3(blocks < 4096 ? static_cast<unsigned>(blocks) : 4096u, a.st.n_seqs), kThreads, 0, st>>>(a);
+      FASTNN_CUDA_TRY(cudaGetLastError());
       const unsigned z = static_cast<unsigned>((a.slab + kTile - 1) / kTile) * a.st.n_seqs;
-      score_chunk_kernel<T><<<dim3(page_blocks, a.st.heads, z), kThreads, 0, st>>>(a);
+      FASTNN_CUDA_TRY(launch_after(score_chunk_kernel<T>, dim3(page_blocks, a.st.heads, z), dim3(kThreads), st, a));
     }
-    FASTNN_CUDA_TRY(cudaGetLastError());
     const int width = a.st.width;
     FASTNN_CUDA_TRY(width <= 128    ? (pick<1, 4>(a, st))
                     : width <= 256  ? (pick<1, 8>(a, st))
@@ -387,6 +424,11 @@ int select_t(const SelectArgs& all, cudaStream_t st) {
 
 size_t select_key_bytes(const StoreArgs& st, int max_new) {
   return static_cast<size_t>(st.n_seqs) * slab_tokens(st, max_new) * st.heads * st.width * 8;
+}
+
+size_t select_sum_bytes(const StoreArgs& st, int max_new) {
+  return max_new < kStepTokens
+             ? 0 : static_cast<size_t>(st.n_seqs) * slab_tokens(st, max_new) * st.heads * st.d * 8;
 }
 
 int launch_select(const SelectArgs& a, int dtype, cudaStream_t st) {

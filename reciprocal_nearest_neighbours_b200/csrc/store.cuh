@@ -60,6 +60,7 @@ struct SelectArgs {
   int keep_first, keep_last, select;
   int32_t* out;
   uint64_t* keys;   // [n_seqs][slab][heads][width] of the slab's tokens
+  double* sums;     // [n_seqs][slab][heads][d], chunks only
   int slab, first;  // tokens of a slab; first token (of each sequence) of this one
 };
 
@@ -156,6 +157,7 @@ size_t attend_tc_floats(const AttendArgs& a);
 int launch_attend_tc(const AttendArgs& a, int dtype, cudaStream_t st);
 int launch_select(const SelectArgs& a, int dtype, cudaStream_t st);
 size_t select_key_bytes(const StoreArgs& st, int max_new);
+size_t select_sum_bytes(const StoreArgs& st, int max_new);
 uint64_t wait_timeout_ns();  // the limit set by fastnn_set_wait_timeout_ns (0: the default)
 
 }  // namespace fastnn

@@ -201,7 +201,9 @@ int fastnn_attend(const fastnn_store* store, const void* q, int64_t q_stride, in
 
 size_t fastnn_select_workspace_size(const fastnn_store* store, int64_t n, int heads_q, int max_new) {
   if (attend_sizes(store, n, heads_q, max_new, 1) != FASTNN_OK) return 0;
-  return n == 0 ? kAlign : align_up(select_key_bytes(store_args(store), max_new));
+  if (n == 0) return kAlign;
+  const StoreArgs a = store_args(store);
+  return align_up(select_key_bytes(a, max_new)) + align_up(select_sum_bytes(a, max_new));
 }
 
 int fastnn_select_pages(const fastnn_store* store, const void* q, int64_t q_stride, int64_t n,
@@ -231,6 +233,8 @@ int fastnn_select_pages(const fastnn_store* store, const void* q, int64_t q_stri
   a.select = select;
   a.out = out_pages;
   a.keys = static_cast<uint64_t*>(workspace);
+  a.sums = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) +
+                                     align_up(select_key_bytes(a.st, max_new)));
   return launch_select(a, store->dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
