@@ -416,7 +416,8 @@ int fastnn_store_append(const fastnn_store *store, const void *k, int64_t k_stri
  *   of the pages listed for its key head. Entries outside its sequence's pages
  *   are skipped; a page that is listed twice counts twice.
  *   workspace: fastnn_attend_workspace_size() with the same arguments (256-byte
- *   aligned). n == 0 is a no-op.
+ *   aligned); where that is 256, for the status word alone, it may be NULL.
+ *   n == 0 is a no-op.
  */
 size_t fastnn_attend_workspace_size(const fastnn_store *store, int64_t n, int heads_q,
                                     int max_new, int select);
@@ -439,7 +440,8 @@ int fastnn_attend(const fastnn_store *store, const void *q, int64_t q_stride, in
  *   token's own future out of the choice, so 1 <= keep_last; keep_first +
  *   keep_last <= select <= 256. store->v_pages and k_pages are not read (may
  *   be NULL); dv is not used but must be valid.
- *   workspace: fastnn_select_workspace_size() bytes, 256-byte aligned.
+ *   workspace: fastnn_select_workspace_size() bytes, 256-byte aligned; may be
+ *   NULL where that is 256.
  */
 size_t fastnn_select_workspace_size(const fastnn_store *store, int64_t n, int heads_q,
                                     int max_new);

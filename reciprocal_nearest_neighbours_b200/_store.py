@@ -36,6 +36,8 @@ _CODES = {torch.bfloat16: FASTNN_BF16, torch.float16: FASTNN_F16}
 _STORE = struct.Struct("@PPPPPPqiiiiiii")
 _ROTATION = struct.Struct("@PPiiif")
 
+_STATUS = 256  # bytes of a workspace that holds nothing but the status word
+
 _bound = None
 _I32 = torch.int32
 
@@ -153,17 +155,18 @@ def _new(shape, dtype, dev, stream):
     return t
 
 
-def _scratch(need: int, dev, workspace, what: str, stream):
-    """The call's workspace and its size."""
+def _scratch(need: int, dev, workspace, what: str, stream) -> int:
+    """Address of the call's workspace, 0 for none: _STATUS bytes hold no more than the status
+    word, which nobody reads where the caller brings no workspace."""
     if need == 0:
         raise FastNNError(-1, what)
     if workspace is None:
-        return _new(need, torch.uint8, dev, stream)
+        return 0 if need == _STATUS else _new(need, torch.uint8, dev, stream).data_ptr()
     if workspace.get_device() != dev:
         raise ValueError(f"the workspace is on {workspace.device}, the tokens on cuda:{dev}")
     if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
         raise FastNNError(-3, "workspace")
-    return workspace
+    return workspace.data_ptr()
 
 
 def _rotation(pos, freq, layout, scale, n, dev) -> bytes:
@@ -255,7 +258,7 @@ def fastnn_store_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
     rot = None if pos is None else _rotation(pos, freq, layout, scale, n, dev)
     ws = None
     if workspace is not None:
-        ws = _scratch(FASTNN_STORE_APPEND_WORKSPACE, dev, workspace, "", stream).data_ptr()
+        ws = _scratch(FASTNN_STORE_APPEND_WORKSPACE, dev, workspace, "", stream)
     _bound or _lib()
     _launch("fastnn_store_append", dev, stream, store, k.data_ptr(), ks, at_v, vs, n, max_new, rot,
             ws, FASTNN_STORE_APPEND_WORKSPACE)
@@ -314,7 +317,7 @@ def fastnn_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     ws = _scratch(need, dev, workspace, "fastnn_attend_workspace_size", stream)
     _launch("fastnn_attend", dev, stream, store, q.data_ptr(), qs, n, hq, max_new, causal,
             d ** -0.5 if scale is None else scale, listed, select, out.data_ptr(), lse.data_ptr(),
-            ws.data_ptr(), need)
+            ws, need)
     return out, lse
 
 
@@ -349,5 +352,5 @@ def fastnn_select_pages(q: torch.Tensor, k_mean: torch.Tensor, page_table: torch
     need = (_bound or _lib()).fastnn_select_workspace_size(store, n, hq, max_new)
     ws = _scratch(need, dev, workspace, "fastnn_select_workspace_size", stream)
     _launch("fastnn_select_pages", dev, stream, store, q.data_ptr(), qs, n, hq, max_new, causal,
-            keep_first, keep_last, select, out.data_ptr(), ws.data_ptr(), need)
+            keep_first, keep_last, select, out.data_ptr(), ws, need)
     return out

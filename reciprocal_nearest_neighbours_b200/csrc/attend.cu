@@ -9,7 +9,8 @@
 // and one split of the positions. Its warps do not wait for one another: each
 // streams every kWarps-th unit of 16 positions through its own cp.async ring,
 // keeps its own (m, l, O), and the warps merge once at the end. Splits leave
-// normalised partial outputs with their log2 sums, which combine_kernel weighs.
+// normalised partial outputs with their log2 sums, which combine_kernel weighs;
+// of selected pages, which are few, the splits are one cluster.
 // The products are mma.sync m16n8k16 with the KEYS as the 16 rows of the first
 // operand and the query rows as its 8 columns: S^T = K Q^T, O^T = V^T P^T. A group
 // of up to 8 heads then wastes no product, O takes half the registers that a
@@ -27,7 +28,15 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 16;    // positions of a unit: the smallest page
-constexpr int kStages = 2;   // units in a warp's ring
+// Units in a warp's ring, and blocks an SM holds. At 128 elements two blocks with
+// deeper rings stream single tokens' keys faster (3 long sequences 120 us against
+// 125 with three blocks of two units), three serve many tokens' pages out of L2
+// faster (2k tokens 280 us against 360).
+template <int DP, bool MANY>
+struct Depth {
+  static constexpr int kStages = DP == 128 ? (MANY ? 2 : 3) : 4;
+  static constexpr int kBlocks = DP == 128 && !MANY ? 2 : 3;
+};
 constexpr float kMostSum = 256.f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -96,7 +105,7 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 }
 
 // NT: groups of 8 query rows of a block.
-template <int DP, int NT>
+template <int DP, int NT, int kStages>
 struct RowsSmem {
   static constexpr int kRows = 8 * NT;
   static constexpr int kTile = kUnit * DP * 2;       // bytes of one K or V unit
@@ -111,22 +120,25 @@ struct RowsSmem {
 // DP: head width padded to 32, 64 or 128. SEL: the positions are those of
 // a.pages' entries for the block's (single) token. FULL: d == dv == DP, so a
 // unit's K and V are 16 * DP consecutive elements each.
-template <typename T, int DP, int NT, bool SEL, bool FULL>
-__global__ void __launch_bounds__(kThreads, 3)
+// With SEL the a.splits blocks of a row tile are a cluster and join their
+// parts through one another's shared memory.
+template <typename T, int DP, int NT, bool SEL, bool FULL, bool MANY>
+__global__ void __launch_bounds__(kThreads, Depth<DP, MANY>::kBlocks)
 attend_rows_kernel(AttendArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
-  using S = RowsSmem<DP, NT>;
+  constexpr int kStages = Depth<DP, MANY>::kStages;
+  using S = RowsSmem<DP, NT, kStages>;
   constexpr int kRows = S::kRows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int s = blockIdx.z, g = blockIdx.y;
   const int split = static_cast<int>(blockIdx.x) % a.splits;
   const int tile = static_cast<int>(blockIdx.x) / a.splits;
-  if (blockIdx.x == 0 && g == 0 && s == 0 && tid == 0) *a.status = 0;
+  if (a.status && blockIdx.x == 0 && g == 0 && s == 0 && tid == 0) *a.status = 0;
   const StoreArgs& st = a.st;
   const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
 
   // The block's rows: row r is token tok(r) of the sequence, query head
-  // head(r); nrows of the 16 exist.
+  // head(r); nrows of kRows exist.
   int r0, nrows, tok_first;
   if constexpr (SEL) {
     const int per_tok = (a.group + kRows - 1) / kRows;
@@ -145,14 +157,15 @@ attend_rows_kernel(AttendArgs a) {
   const int vmax = visible(w, last);  // visible() grows with the token
 
   int u_count;      // units of the whole block
+  int u_first = 0;  // SEL: the first of them
   int k0 = 0;       // first position (not SEL)
   const int32_t* list = nullptr;
   const int upp = st.page / kUnit;
   if constexpr (SEL) {
-    const int e0 = split * a.split_len;
-    const int e1 = e0 + a.split_len < a.select ? e0 + a.split_len : a.select;
-    list = a.pages + ((static_cast<int64_t>(w.t0) + tok_first) * st.heads + g) * a.select + e0;
-    u_count = e1 > e0 ? (e1 - e0) * upp : 0;
+    list = a.pages + ((static_cast<int64_t>(w.t0) + tok_first) * st.heads + g) * a.select;
+    const int u1 = a.select * upp;  // split_len counts units here
+    u_first = split * a.split_len;
+    u_count = u1 - u_first < a.split_len ? u1 - u_first : a.split_len;
   } else {
     k0 = split * a.split_len;
     if (split > 0 && k0 >= vmax) return;  // no row of the tile reads this split
@@ -200,7 +213,7 @@ attend_rows_kernel(AttendArgs a) {
     if (u < u_count) {
       int lp;
       if constexpr (SEL) {
-        lp = __ldg(list + u / upp);
+        lp = __ldg(list + (u_first + u) / upp);
       } else {
         lp = (k0 + u * kUnit) >> st.page_log2;
       }
@@ -214,7 +227,7 @@ attend_rows_kernel(AttendArgs a) {
   // First position of unit j of this warp; its id decides whether it exists.
   auto unit_pos = [&](int j, int lp) {
     const int u = warp + j * kWarps;
-    if constexpr (SEL) return lp * st.page + (u % upp) * kUnit;
+    if constexpr (SEL) return lp * st.page + ((u_first + u) & (upp - 1)) * kUnit;
     return k0 + u * kUnit;
   };
   // Copies of one unit, 16 bytes a lane and step: step i takes chunk c of row
@@ -413,52 +426,95 @@ attend_rows_kernel(AttendArgs a) {
     }
   __syncthreads();
   constexpr int kPerRow = kThreads / kRows;  // threads a row
-  const int r = tid / kPerRow;
-  if (r >= nrows) return;
+  constexpr int kVec = (DP + kPerRow * 4 - 1) / (kPerRow * 4);
+  const int r = tid / kPerRow, c_first = (tid % kPerRow) * 4;
   float top = -INFINITY;
 #pragma unroll
   for (int q = 0; q < kWarps; ++q) top = fmaxf(top, ml[(q * kRows + r) * 2]);
-  float f[kWarps], sum = 0.f;
+  float sum = 0.f;
+  float4 v[kVec];
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int q = 0; q < kWarps; ++q) {
     const float mq = ml[(q * kRows + r) * 2];
-    f[q] = mq == -INFINITY ? 0.f : mq == top ? 1.f : ex2(mq - top);
-    sum += f[q] * ml[(q * kRows + r) * 2 + 1];
+    const float f = mq == -INFINITY ? 0.f : mq == top ? 1.f : ex2(mq - top);
+    sum += f * ml[(q * kRows + r) * 2 + 1];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const int c = c_first + k * kPerRow * 4;
+      if (c >= DP) break;
+      const float4 y = *reinterpret_cast<const float4*>(
+          reinterpret_cast<const float*>(smem + q * S::kRing) + r * S::kOutPitch + c);
+      v[k].x += f * y.x;
+      v[k].y += f * y.y;
+      v[k].z += f * y.z;
+      v[k].w += f * y.w;
+    }
   }
+  if (SEL && a.splits > 1) {
+    // This block's part goes where the first warp's was; then each thread joins
+    // the parts of its places, the blocks taking turns at the columns.
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const int c = c_first + k * kPerRow * 4;
+      if (c < DP) *reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + r * S::kOutPitch + c) = v[k];
+    }
+    if (tid % kPerRow == 0) {
+      ml[r * 2] = top;
+      ml[r * 2 + 1] = sum;
+    }
+    ptx::cluster_sync();
+    const uint32_t base = ptx::smem_u32(smem), mls = ptx::smem_u32(ml) + r * 8;
+    top = -INFINITY;
+    for (int q = 0; q < a.splits; ++q) top = fmaxf(top, ptx::cluster_ld2(ptx::cluster_map(mls, q)).x);
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = 0; q < a.splits; ++q) {
+      const float2 part = ptx::cluster_ld2(ptx::cluster_map(mls, q));
+      const float f = part.x == -INFINITY ? 0.f : part.x == top ? 1.f : ex2(part.x - top);
+      sum += f * part.y;
+      const uint32_t from = ptx::cluster_map(base, q) + r * S::kOutPitch * 4;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        const int c = c_first + k * kPerRow * 4;
+        if (c >= st.dv || (c / 4) % a.splits != split) continue;
+        const float4 y = ptx::cluster_ld4(from + c * 4);
+        v[k].x += f * y.x;
+        v[k].y += f * y.y;
+        v[k].z += f * y.z;
+        v[k].w += f * y.w;
+      }
+    }
+    ptx::cluster_sync();  // no block leaves while others read its part
+  }
+  if (r >= nrows) return;
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
   const float lse2 = sum > 0.f ? top + log2f(sum) : sum == 0.f ? -INFINITY : sum;
   const int rr = r0 + r;
   const int tok = SEL ? tok_first : rr / a.group;
   const int hd = g * a.group + (SEL ? rr : rr - tok * a.group);
   const int64_t row = (static_cast<int64_t>(w.t0) + tok) * a.hq + hd;
-  const bool whole = SEL ? a.splits == 1 : visible(w, tok) <= a.split_len;
-  if (whole && split > 0) return;
-  for (int c = (tid % kPerRow) * 4; c < st.dv; c += kPerRow * 4) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool whole = SEL || visible(w, tok) <= a.split_len;
+  if (!SEL && whole && split > 0) return;
 #pragma unroll
-    for (int q = 0; q < kWarps; ++q) {
-      const float4 y = *reinterpret_cast<const float4*>(
-          reinterpret_cast<const float*>(smem + q * S::kRing) + r * S::kOutPitch + c);
-      v.x += f[q] * y.x;
-      v.y += f[q] * y.y;
-      v.z += f[q] * y.z;
-      v.w += f[q] * y.w;
-    }
-    v.x *= inv;
-    v.y *= inv;
-    v.z *= inv;
-    v.w *= inv;
+  for (int k = 0; k < kVec; ++k) {
+    const int c = c_first + k * kPerRow * 4;
+    if (c >= st.dv || (SEL && a.splits > 1 && (c / 4) % a.splits != split)) continue;
+    const float4 y = make_float4(v[k].x * inv, v[k].y * inv, v[k].z * inv, v[k].w * inv);
     if (whole) {
       *reinterpret_cast<uint2*>(a.out + row * st.dv + c) =
-          make_uint2(Half16<T>::pack(v.x, v.y), Half16<T>::pack(v.z, v.w));
+          make_uint2(Half16<T>::pack(y.x, y.y), Half16<T>::pack(y.z, y.w));
     } else {
-      *reinterpret_cast<float4*>(a.part + (split * a.n * a.hq + row) * st.dv + c) = v;
+      *reinterpret_cast<float4*>(a.part + (split * a.n * a.hq + row) * st.dv + c) = y;
     }
   }
   if (tid % kPerRow == 0) {
     if (!whole) {
       a.part_lse[split * a.n * a.hq + row] = lse2;
-    } else if (a.lse) {
+    } else if (a.lse && (!SEL || split == 0)) {
       a.lse[row] = lse2 * 0.69314718055994530942f;  // ln 2
     }
   }
@@ -466,7 +522,7 @@ attend_rows_kernel(AttendArgs a) {
 
 // Joins the splits of each row: out = sum_i 2^(lse2_i - lse2) out_i. A warp
 // takes one row.
-template <typename T, bool SEL>
+template <typename T>
 __global__ void __launch_bounds__(128)
 combine_kernel(AttendArgs a) {
   cudaGridDependencySynchronize();
@@ -477,7 +533,7 @@ combine_kernel(AttendArgs a) {
   if (r >= static_cast<int64_t>(w.n) * a.hq) return;
   const int tok = static_cast<int>(r / a.hq);
   const int vis = visible(w, tok);
-  const int parts = SEL ? a.splits : (vis + a.split_len - 1) / a.split_len;
+  const int parts = (vis + a.split_len - 1) / a.split_len;
   if (parts <= 1) return;  // its one split has written the result
   const int64_t row = static_cast<int64_t>(w.t0) * a.hq + r;
   const int64_t step = a.n * a.hq;
@@ -525,31 +581,47 @@ int64_t row_tiles(const AttendArgs& a) {
                  : (static_cast<int64_t>(a.max_new) * a.group + per - 1) / per;
 }
 
-template <typename T, int DP, int NT, bool SEL, bool FULL>
+template <typename T, int DP, int NT, bool SEL, bool FULL, bool MANY>
 int rows_launch(const AttendArgs& a, cudaStream_t st) {
-  using S = RowsSmem<DP, NT>;
-  static_assert(3 * (S::kTotal + 1024) <= 228 * 1024, "three blocks fit an SM");
-  FASTNN_CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<T, DP, NT, SEL, FULL>,
+  using D = Depth<DP, MANY>;
+  using S = RowsSmem<DP, NT, D::kStages>;
+  static_assert(D::kBlocks * (S::kTotal + 1024) <= 228 * 1024, "the blocks fit an SM");
+  FASTNN_CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<T, DP, NT, SEL, FULL, MANY>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal));
   const int64_t tiles = row_tiles(a);
   if (tiles * a.splits > INT32_MAX) return FASTNN_ERR_INVALID;
   const dim3 grid(static_cast<unsigned>(tiles * a.splits), a.st.heads, a.st.n_seqs);
-  attend_rows_kernel<T, DP, NT, SEL, FULL><<<grid, kThreads, S::kTotal, st>>>(a);
+  if (SEL && a.splits > 1) {
+    FASTNN_CUDA_TRY(launch_cluster(attend_rows_kernel<T, DP, NT, SEL, FULL, MANY>, grid, dim3(kThreads), S::kTotal,
+                                   a.splits, st, a));
+    return FASTNN_OK;
+  }
+  attend_rows_kernel<T, DP, NT, SEL, FULL, MANY><<<grid, kThreads, S::kTotal, st>>>(a);
   FASTNN_CUDA_TRY(cudaGetLastError());
   if (a.splits > 1) {
     const int64_t blocks = (static_cast<int64_t>(a.max_new) * a.hq + 3) / 4;
-    FASTNN_CUDA_TRY(launch_after(combine_kernel<T, SEL>, dim3(static_cast<unsigned>(blocks), a.st.n_seqs),
+    FASTNN_CUDA_TRY(launch_after(combine_kernel<T>, dim3(static_cast<unsigned>(blocks), a.st.n_seqs),
                                  dim3(128), st, a));
   }
   return FASTNN_OK;
+}
+
+template <typename T, int DP, int NT, bool SEL, bool FULL>
+int rows_many(const AttendArgs& a, cudaStream_t st) {
+  // More row tiles than the deeper rings' blocks fill twice: their keys are
+  // shared, and come out of L2.
+  if constexpr (DP == 128)
+    if (row_tiles(a) * a.st.heads * a.st.n_seqs > 4 * 148 && a.max_new > 1)
+      return rows_launch<T, DP, NT, SEL, FULL, true>(a, st);
+  return rows_launch<T, DP, NT, SEL, FULL, false>(a, st);
 }
 
 template <typename T, int DP, bool SEL>
 int rows_full(const AttendArgs& a, cudaStream_t st) {
   const bool full = a.st.d == DP && a.st.dv == DP;
   if (row_groups(a) == 1)
-    return full ? rows_launch<T, DP, 1, SEL, true>(a, st) : rows_launch<T, DP, 1, SEL, false>(a, st);
-  return full ? rows_launch<T, DP, 2, SEL, true>(a, st) : rows_launch<T, DP, 2, SEL, false>(a, st);
+    return full ? rows_many<T, DP, 1, SEL, true>(a, st) : rows_many<T, DP, 1, SEL, false>(a, st);
+  return full ? rows_many<T, DP, 2, SEL, true>(a, st) : rows_many<T, DP, 2, SEL, false>(a, st);
 }
 
 template <typename T, bool SEL>
@@ -564,22 +636,24 @@ int rows_width(const AttendArgs& a, cudaStream_t st) {
 
 // How many blocks share the positions of a row tile. The lengths are on the
 // device; the table's width bounds them. About four waves of blocks (two a SM)
-// even out ragged lengths, a split is at least 256 positions (four pages of a
-// selection) long, and splits beyond a row's length cost an empty block each.
+// even out ragged lengths, a split is at least 256 positions long, and splits
+// beyond a row's length cost an empty block each.
 void attend_plan(AttendArgs& a) {
   const bool sel = a.pages != nullptr;
   const int64_t tiles = row_tiles(a);
   const int64_t base = tiles * a.st.heads * a.st.n_seqs;
-  const int64_t want = 4 * 2 * 148;
-  int64_t splits = base >= want ? 1 : (want + base - 1) / base;
   if (sel) {
-    const int64_t most = (a.select + 3) / 4;
-    if (base >= 148) splits = 1;  // entries are of one length: a wave is enough
-    if (splits > most) splits = most;
-    a.split_len = static_cast<int>((a.select + splits - 1) / splits);
-    a.splits = (a.select + a.split_len - 1) / a.split_len;
+    // One wave of blocks (units are of one length), joined as clusters of up to 8.
+    const int units = a.select * (a.st.page / kUnit);
+    int64_t splits = base >= 2 * 148 ? 1 : 2 * 148 / base;
+    if (splits > 8) splits = 8;
+    if (splits > (units + 15) / 16) splits = (units + 15) / 16;  // four units a warp at least
+    a.split_len = static_cast<int>((units + splits - 1) / splits);
+    a.splits = (units + a.split_len - 1) / a.split_len;
     return;
   }
+  const int64_t want = 4 * 2 * 148;
+  const int64_t splits = base >= want ? 1 : (want + base - 1) / base;
   const int64_t cap = static_cast<int64_t>(a.st.width) * a.st.page;
   int64_t len = (cap + splits - 1) / splits;
   if (len < 256) len = 256;

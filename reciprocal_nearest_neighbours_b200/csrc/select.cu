@@ -6,17 +6,19 @@
 // The choice among nearly equal scores has to be the definition's, not the
 // summation order's, so scores are formed in fp64: the sum of the group's
 // queries is exact or nearly so, the products are, and the sums agree to about
-// 1e-16 whatever their order. A score kernel writes order-preserving 64-bit
-// keys (0: not a candidate, all ones: taken whatever its score):
-//   steps (fewer than kTile tokens a sequence): half a warp a page, 16 bytes a
-//       lane; bound by reading the means once, spread over all SMs;
-//   chunks: the groups' sums once by a kernel of their own, then tiles of 64
-//       tokens x 64 pages, 4 x 4 a thread, both operands as fp64 in shared memory;
-//       bound by the fp64 units and the shared memory that feeds them.
-// A pick kernel then holds a row's keys in registers, finds the select-th
-// largest bit by bit (from the highest bit in which the row's keys differ), and
-// writes the pages in ascending order. The keys of a slab of tokens stay below
-// kSlabBytes, about half of L2.
+// 1e-16 whatever their order. They become order-preserving 64-bit keys (0: not
+// a candidate, all ones: taken whatever its score); a row's keys are held in
+// registers, the select-th largest is found bit by bit (from the highest bit
+// in which they differ), and the pages are written in ascending order.
+//   steps (a few tokens a sequence): half a warp scores a page; up to 512 pages
+//       by the block that picks, more by blocks of 64 pages before the choice.
+//       Bound by latency, then by reading the means once. (A cluster of 8 blocks
+//       that shares the pages and picks in one kernel took 30 us for 16
+//       sequences of up to 1024 pages; the two kernels take 24.)
+//   chunks: the groups' sums once, then tiles of 64 tokens x 64 pages, 4 x 4 a
+//       thread, both operands as fp64 in shared memory (bound by the fp64 units
+//       and the shared memory that feeds them), then the choice. The keys of a
+//       slab of tokens stay below kSlabBytes, about half of L2.
 #include "store.cuh"
 
 namespace fastnn {
@@ -26,7 +28,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 64;      // tokens, pages of a score tile
 constexpr int kDepth = 32;     // elements of d in shared memory at a time
-constexpr int kStepTokens = 8; // fewer new tokens a sequence: the step kernel
+constexpr int kStepTokens = 8; // fewer new tokens a sequence: the step kernel (a block each)
+constexpr int kWholeWidth = 512;  // pages that a step's block scores and picks from by itself
+constexpr int kShare = 64;        // pages that it scores where the table is wider
 constexpr int64_t kSlabBytes = 64 << 20;
 
 __device__ __forceinline__ uint64_t key_of(double x) {
@@ -56,60 +60,253 @@ __device__ __forceinline__ int page_of(const SelectArgs& a, int s, int p) {
   return id < a.st.n_pages ? id : -1;
 }
 
-// Block: 64 pages of one sequence and key head; a warp takes 8 of them, half a
-// warp one, lane l % 16 elements 8 (l % 16) and on.
-template <typename T>
+// Picks the pages of one row from its keys. W warps a row; thread r of the row
+// holds keys [r * K, r * K + K) in registers (K == 0: any number, read again and
+// again from `keys`).
+template <int W, int K>
+__device__ __forceinline__ void pick_row(const SelectArgs& a, const uint64_t* keys,
+                                         const uint64_t (&held)[K ? K : 1], int seen, int64_t token, int g) {
+  constexpr int kRow = 32 * W;
+  __shared__ int parts[2][8];
+  __shared__ uint64_t ends[2][8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = W == 1 ? lane : tid;
+  const int per = K ? K : (seen + kRow - 1) / kRow;
+  const int p0 = r * per;
+  auto key = [&](int k) -> uint64_t { return p0 + k < seen ? keys[p0 + k] : 0; };
+  int turn = 0;
+  auto total = [&](int c) {  // over the row
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (W > 1) {
+      if (lane == 0) parts[turn][warp] = c;
+      __syncthreads();
+      c = 0;
+#pragma unroll
+      for (int q = 0; q < W; ++q) c += parts[turn][q];
+      turn ^= 1;
+    }
+    return c;
+  };
+  auto before = [&](int c) {  // over the threads of the row before this one
+    int x = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int all = __shfl_sync(0xffffffffu, x, 31);
+    x -= c;
+    if (W > 1) {
+      if (lane == 0) parts[turn][warp] = all;
+      __syncthreads();
+      for (int q = 0; q < warp; ++q) x += parts[turn][q];
+      turn ^= 1;
+    }
+    return x;
+  };
+  auto count = [&](uint64_t level) {
+    int c = 0;
+    if (K) {
+#pragma unroll
+      for (int k = 0; k < (K ? K : 1); ++k) c += held[k] >= level;
+    } else {
+      for (int k = 0; k < per; ++k) c += key(k) >= level;
+    }
+    return total(c);
+  };
+  // The largest level that at least `select` keys reach (1: every candidate is
+  // taken), and how many of the keys equal to it are (room < 0: all).
+  uint64_t level = 1;
+  int room = -1;
+  if (count(1) > a.select) {
+    // Bits above the highest one in which the candidates by score differ are common.
+    uint64_t lo = ~0ull, hi = 0;
+    for (int k = 0; k < per; ++k) {
+      const uint64_t x = K ? held[K ? k : 0] : key(k);
+      if (x && x != ~0ull) {  // those taken in any case reach every level
+        lo = x < lo ? x : lo;
+        hi = x > hi ? x : hi;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const uint64_t l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
+      lo = l2 < lo ? l2 : lo;
+      hi = h2 > hi ? h2 : hi;
+    }
+    if (W > 1) {
+      if (lane == 0) {
+        ends[0][warp] = lo;
+        ends[1][warp] = hi;
+      }
+      __syncthreads();
+      for (int q = 0; q < W; ++q) {
+        lo = ends[0][q] < lo ? ends[0][q] : lo;
+        hi = ends[1][q] > hi ? ends[1][q] : hi;
+      }
+    }
+    level = hi;
+    int reach = a.select;
+    if (lo != hi) {
+      const int top = 63 - __clzll(static_cast<long long>(lo ^ hi));
+      level = top == 63 ? 0 : (hi >> (top + 1)) << (top + 1);
+      reach = a.select + 1;  // more than select keys reach the common bits
+      for (int b = top; b >= 0; --b) {
+        const uint64_t up = level | (1ull << b);
+        const int c = count(up);
+        if (c >= a.select) {
+          level = up;
+          reach = c;
+          if (c == a.select) break;
+        }
+      }
+    } else {
+      reach = a.select + 1;
+    }
+    if (reach > a.select) room = a.select - (level == ~0ull ? 0 : count(level + 1));
+  }
+  int ties = 0, more = 0;
+  if (room >= 0) {
+    for (int k = 0; k < per; ++k) ties += (K ? held[K ? k : 0] : key(k)) == level;
+    ties = before(ties);  // equal keys in the threads before
+  }
+  int t = ties;
+  for (int k = 0; k < per; ++k) {
+    const uint64_t x = K ? held[K ? k : 0] : key(k);
+    more += x > level || (x == level && (room < 0 || t < room));
+    t += x == level;
+  }
+  int at = before(more);
+  int32_t* out = a.out + (token * a.st.heads + g) * a.select;
+  t = ties;
+  for (int k = 0; k < per; ++k) {
+    const uint64_t x = K ? held[K ? k : 0] : key(k);
+    const bool take = x > level || (x == level && (room < 0 || t < room));
+    t += x == level;
+    if (take && at < a.select) out[at++] = p0 + k;
+  }
+  const int taken = total(more);
+  for (int k = taken + r; k < a.select; k += kRow) out[k] = -1;
+}
+
+template <int W, int K>
 __global__ void __launch_bounds__(kThreads)
-score_step_kernel(SelectArgs a) {
-  __shared__ double qs[128];
+pick_kernel(SelectArgs a) {
+  cudaGridDependencySynchronize();
+  const StoreArgs& st = a.st;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = W == 1 ? static_cast<int64_t>(blockIdx.x) * 8 + warp : blockIdx.x;
+  const int g = static_cast<int>(row % st.heads);
+  const int64_t si = row / st.heads;
+  const int s = static_cast<int>(si / a.slab), i = static_cast<int>(si - static_cast<int64_t>(s) * a.slab);
+  if (s >= st.n_seqs) return;
+  const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
+  if (a.first + i >= w.n) return;
+  const int seen = seen_pages(a, w, a.first + i);
+  const uint64_t* keys = key_row(a, s, i, g);
+  uint64_t held[K ? K : 1];
+  if (K) {
+    const int p0 = (W == 1 ? lane : tid) * K;
+#pragma unroll
+    for (int k = 0; k < K; ++k) held[k] = p0 + k < seen ? keys[p0 + k] : 0;
+  }
+  pick_row<W, K>(a, keys, held, seen, static_cast<int64_t>(w.t0) + a.first + i, g);
+}
+
+// Steps: half a warp a page, lane l % 16 elements 8 (l % 16) and on, for each of the
+// (fewer than kStepTokens) tokens. WHOLE: a block scores all pages of its sequence
+// and key head and picks from them; else it scores kShare pages, and pick_kernel
+// follows.
+template <typename T, bool WHOLE>
+__global__ void __launch_bounds__(kThreads)
+step_kernel(SelectArgs a) {
+  __shared__ uint64_t held_keys[WHOLE ? kStepTokens * kWholeWidth : 1];
+  __shared__ __align__(16) double qs[kStepTokens][128];
   const StoreArgs& st = a.st;
   const int s = blockIdx.z, g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
-  const int n = w.n - a.first < a.slab ? w.n - a.first : a.slab;
-  if (n <= 0) return;
-  const int p0 = blockIdx.x * 64 + warp * 8 + (lane >> 4);
-  const int last = seen_pages(a, w, a.first + n - 1);
-  if (static_cast<int>(blockIdx.x) * 64 >= last) return;
+  if (w.n <= 0) return;
+  const int last = seen_pages(a, w, w.n - 1);
+  const int share = WHOLE ? kWholeWidth : kShare, first = static_cast<int>(blockIdx.x) * share;
+  if (!WHOLE && first >= last) return;
   const int e0 = (lane & 15) * 8;
-  uint4 mean[4];
-  bool there[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int p = p0 + 2 * k;
-    const int id = p < last ? page_of(a, s, p) : -1;
-    there[k] = id >= 0;
+  constexpr int kFly = 4;  // pages in flight a half warp
+  uint4 mean[kFly];
+  int id[kFly];
+  auto fetch = [&](int k, int p) {
+    id[k] = p < first + share && p < last ? page_of(a, s, p) : -1;
     mean[k] = make_uint4(0, 0, 0, 0);
-    if (there[k] && e0 < st.d)
-      mean[k] = __ldg(reinterpret_cast<const uint4*>(st.mean + (static_cast<int64_t>(id) * st.heads + g) * st.d + e0));
-  }
-  for (int i = 0; i < n; ++i) {
-    __syncthreads();
-    if (tid < 128) {
-      double sum = 0.0;
-      if (tid < st.d) {
-        const uint16_t* q = a.q + (static_cast<int64_t>(w.t0) + a.first + i) * a.q_stride +
-                            static_cast<int64_t>(g) * a.group * st.d + tid;
-        for (int h = 0; h < a.group; ++h) sum += static_cast<double>(Half16<T>::one(__ldg(q + h * st.d)));
-      }
-      qs[tid] = sum;
-    }
-    __syncthreads();
-    const int seen = seen_pages(a, w, a.first + i);
-    uint64_t* keys = key_row(a, s, i, g);
+    if (id[k] >= 0 && e0 < st.d)
+      mean[k] = __ldg(reinterpret_cast<const uint4*>(
+          st.mean + (static_cast<int64_t>(id[k]) * st.heads + g) * st.d + e0));
+  };
+  const int half = lane >> 4;
+  int pw = first + warp * 2;  // the warp's first page: its two halves go through the loop together
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t xs[4] = {mean[k].x, mean[k].y, mean[k].z, mean[k].w};
-      double acc = 0.0;
+  for (int k = 0; k < kFly; ++k) fetch(k, pw + half + 16 * k);
+  for (int x = tid; x < w.n * 128; x += kThreads) {
+    const int i = x >> 7, e = x & 127;
+    double sum = 0.0;
+    if (e < st.d) {
+      const uint16_t* q = a.q + (static_cast<int64_t>(w.t0) + i) * a.q_stride +
+                          static_cast<int64_t>(g) * a.group * st.d + e;
+      for (int h = 0; h < a.group; ++h) sum += static_cast<double>(Half16<T>::one(__ldg(q + h * st.d)));
+    }
+    qs[i][e] = sum;
+  }
+  __syncthreads();
+  for (; pw < first + share && pw < last; pw += 16 * kFly) {
+    uint4 x[kFly];
+    bool there[kFly];
+#pragma unroll
+    for (int k = 0; k < kFly; ++k) {
+      x[k] = mean[k];
+      there[k] = id[k] >= 0;
+      fetch(k, pw + half + 16 * (kFly + k));
+    }
+    for (int i = 0; i < w.n; ++i) {
+      // The pages' sums side by side: their chains of additions overlap.
+      double acc[kFly] = {};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 f = Half16<T>::unpack(xs[e]);
-        acc += static_cast<double>(f.x) * qs[e0 + 2 * e];
-        acc += static_cast<double>(f.y) * qs[e0 + 2 * e + 1];
+        const double2 q = *reinterpret_cast<const double2*>(&qs[i][e0 + 2 * e]);
+#pragma unroll
+        for (int k = 0; k < kFly; ++k) {
+          const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          const float2 y = Half16<T>::unpack(xs[e]);
+          acc[k] += static_cast<double>(y.x) * q.x;
+          acc[k] += static_cast<double>(y.y) * q.y;
+        }
       }
 #pragma unroll
-      for (int o = 8; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-      const int p = p0 + 2 * k;
-      if ((lane & 15) == 0 && p < seen) keys[p] = candidate(a, p, seen, there[k], acc);
+      for (int o = 8; o; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < kFly; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+      const int seen = seen_pages(a, w, i);
+#pragma unroll
+      for (int k = 0; k < kFly; ++k) {
+        const int p = pw + half + 16 * k;
+        if ((lane & 15) == k && p < first + share && p < seen) {
+          const uint64_t key = candidate(a, p, seen, there[k], acc[k]);
+          if (WHOLE) {
+            held_keys[i * kWholeWidth + p] = key;
+          } else {
+            key_row(a, s, i, g)[p] = key;
+          }
+        }
+      }
+    }
+  }
+  if constexpr (WHOLE) {
+    __syncthreads();
+    constexpr int K = kWholeWidth / kThreads;
+    for (int i = 0; i < w.n; ++i) {
+      const int seen = seen_pages(a, w, i);
+      uint64_t held[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) held[k] = tid * K + k < seen ? held_keys[i * kWholeWidth + tid * K + k] : 0;
+      pick_row<8, K>(a, nullptr, held, seen, static_cast<int64_t>(w.t0) + i, g);
+      __syncthreads();
     }
   }
 }
@@ -223,153 +420,6 @@ score_chunk_kernel(SelectArgs a) {
   }
 }
 
-// W warps a row. Thread r of the row holds keys [r * K, r * K + K) in registers
-// (K == 0: any number, read again and again).
-template <int W, int K>
-__global__ void __launch_bounds__(kThreads)
-pick_kernel(SelectArgs a) {
-  cudaGridDependencySynchronize();
-  constexpr int kRow = 32 * W;
-  __shared__ int parts[2][8];
-  __shared__ uint64_t ends[2][8];
-  const StoreArgs& st = a.st;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = W == 1 ? lane : tid;
-  const int64_t row = W == 1 ? static_cast<int64_t>(blockIdx.x) * 8 + warp : blockIdx.x;
-  const int g = static_cast<int>(row % st.heads);
-  const int64_t si = row / st.heads;
-  const int s = static_cast<int>(si / a.slab), i = static_cast<int>(si - static_cast<int64_t>(s) * a.slab);
-  if (s >= st.n_seqs) return;
-  const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
-  if (a.first + i >= w.n) return;
-  const int seen = seen_pages(a, w, a.first + i);
-  const uint64_t* keys = key_row(a, s, i, g);
-  const int per = K ? K : (seen + kRow - 1) / kRow;
-  const int p0 = r * per;
-  uint64_t held[K ? K : 1];
-  if (K) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) held[k] = p0 + k < seen ? keys[p0 + k] : 0;
-  }
-  auto key = [&](int k) -> uint64_t {
-    if (K) return held[k];
-    return p0 + k < seen ? keys[p0 + k] : 0;
-  };
-  int turn = 0;
-  auto total = [&](int c) {  // over the row
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (W > 1) {
-      if (lane == 0) parts[turn][warp] = c;
-      __syncthreads();
-      c = 0;
-#pragma unroll
-      for (int q = 0; q < W; ++q) c += parts[turn][q];
-      turn ^= 1;
-    }
-    return c;
-  };
-  auto before = [&](int c) {  // over the threads of the row before this one
-    int x = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    const int all = __shfl_sync(0xffffffffu, x, 31);
-    x -= c;
-    if (W > 1) {
-      if (lane == 0) parts[turn][warp] = all;
-      __syncthreads();
-      for (int q = 0; q < warp; ++q) x += parts[turn][q];
-      turn ^= 1;
-    }
-    return x;
-  };
-  auto count = [&](uint64_t level) {
-    int c = 0;
-    if (K) {
-#pragma unroll
-      for (int k = 0; k < (K ? K : 1); ++k) c += held[k] >= level;
-    } else {
-      for (int k = 0; k < per; ++k) c += key(k) >= level;
-    }
-    return total(c);
-  };
-  // The largest level that at least `select` keys reach (1: every candidate is
-  // taken), and how many of the keys equal to it are (room < 0: all).
-  uint64_t level = 1;
-  int room = -1;
-  if (count(1) > a.select) {
-    // Bits above the highest one in which the candidates differ are common.
-    uint64_t lo = ~0ull, hi = 0;
-    for (int k = 0; k < per; ++k) {
-      const uint64_t x = K ? held[K ? k : 0] : key(k);
-      if (x) {
-        lo = x < lo ? x : lo;
-        hi = x > hi ? x : hi;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const uint64_t l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
-      lo = l2 < lo ? l2 : lo;
-      hi = h2 > hi ? h2 : hi;
-    }
-    if (W > 1) {
-      if (lane == 0) {
-        ends[0][warp] = lo;
-        ends[1][warp] = hi;
-      }
-      __syncthreads();
-      for (int q = 0; q < W; ++q) {
-        lo = ends[0][q] < lo ? ends[0][q] : lo;
-        hi = ends[1][q] > hi ? ends[1][q] : hi;
-      }
-    }
-    level = hi;
-    int reach = a.select;
-    if (lo != hi) {
-      const int top = 63 - __clzll(static_cast<long long>(lo ^ hi));
-      level = top == 63 ? 0 : (hi >> (top + 1)) << (top + 1);
-      reach = a.select + 1;  // more than select keys reach the common bits
-      for (int b = top; b >= 0; --b) {
-        const uint64_t up = level | (1ull << b);
-        const int c = count(up);
-        if (c >= a.select) {
-          level = up;
-          reach = c;
-          if (c == a.select) break;
-        }
-      }
-    } else {
-      reach = a.select + 1;
-    }
-    if (reach > a.select) room = a.select - (level == ~0ull ? 0 : count(level + 1));
-  }
-  int ties = 0, more = 0;
-  if (room >= 0) {
-    for (int k = 0; k < per; ++k) ties += (K ? held[K ? k : 0] : key(k)) == level;
-    ties = before(ties);  // equal keys in the threads before
-  }
-  int t = ties;
-  for (int k = 0; k < per; ++k) {
-    const uint64_t x = K ? held[K ? k : 0] : key(k);
-    more += x > level || (x == level && (room < 0 || t < room));
-    t += x == level;
-  }
-  int at = before(more);
-  int32_t* out = a.out + ((static_cast<int64_t>(w.t0) + a.first + i) * st.heads + g) * a.select;
-  t = ties;
-  for (int k = 0; k < per; ++k) {
-    const uint64_t x = K ? held[K ? k : 0] : key(k);
-    const bool take = x > level || (x == level && (room < 0 || t < room));
-    t += x == level;
-    if (take && at < a.select) out[at++] = p0 + k;
-  }
-  const int taken = total(more);
-  for (int k = taken + r; k < a.select; k += kRow) out[k] = -1;
-}
-
 // Tokens of one slab: their keys stay below kSlabBytes (at least one tile).
 int64_t slab_tokens(const StoreArgs& st, int max_new) {
   int64_t n = kSlabBytes / (static_cast<int64_t>(st.n_seqs) * st.heads * st.width * 8);
@@ -386,20 +436,27 @@ cudaError_t pick(const SelectArgs& a, cudaStream_t st) {
   return launch_after(pick_kernel<W, K>, dim3(static_cast<unsigned>(blocks)), dim3(W == 1 ? kThreads : 32 * W), st, a);
 }
 
+bool is_step(int max_new) { return max_new < kStepTokens; }
+// Steps over few pages need no scratch.
+bool is_whole(const StoreArgs& st, int max_new) { return is_step(max_new) && st.width <= kWholeWidth; }
+
 template <typename T>
 int select_t(const SelectArgs& all, cudaStream_t st) {
   SelectArgs a = all;
-  a.slab = static_cast<int>(slab_tokens(a.st, a.max_new));
-  const int tiles = (a.slab + kTile - 1) / kTile;
-  const int page_blocks = (a.st.width + kTile - 1) / kTile;
-  const bool step = a.max_new < kStepTokens;
-  if (!step && static_cast<int64_t>(tiles) * a.st.n_seqs > 65535) {
-    // Too many tiles for one grid dimension: a tile of tokens at a time.
-    a.slab = kTile;
+  const int width = a.st.width;
+  a.first = 0;
+  if (is_whole(a.st, a.max_new)) {
+    step_kernel<T, true><<<dim3(1, a.st.heads, a.st.n_seqs), kThreads, 0, st>>>(a);
+    FASTNN_CUDA_TRY(cudaGetLastError());
+    return FASTNN_OK;
   }
-  for (a.first = 0; a.first < a.max_new; a.first += a.slab) {
-    if (step) {
-      score_step_kernel<T><<<dim3(page_blocks, a.st.heads, a.st.n_seqs), kThreads, 0, st>>>(a);
+  a.slab = static_cast<int>(slab_tokens(a.st, a.max_new));
+  const int page_blocks = (width + kTile - 1) / kTile;
+  // Too many tiles for one grid dimension: a tile of tokens at a time.
+  if (static_cast<int64_t>((a.slab + kTile - 1) / kTile) * a.st.n_seqs > 65535) a.slab = kTile;
+  for (; a.first < a.max_new; a.first += a.slab) {
+    if (is_step(a.max_new)) {
+      step_kernel<T, false><<<dim3((width + kShare - 1) / kShare, a.st.heads, a.st.n_seqs), kThreads, 0, st>>>(a);
       FASTNN_CUDA_TRY(cudaGetLastError());
     } else {
       const int64_t items = static_cast<int64_t>(a.slab) * a.st.heads * (a.st.d / 8);
@@ -409,7 +466,6 @@ int select_t(const SelectArgs& all, cudaStream_t st) {
       const unsigned z = static_cast<unsigned>((a.slab + kTile - 1) / kTile) * a.st.n_seqs;
       FASTNN_CUDA_TRY(launch_after(score_chunk_kernel<T>, dim3(page_blocks, a.st.heads, z), dim3(kThreads), st, a));
     }
-    const int width = a.st.width;
     FASTNN_CUDA_TRY(width <= 128    ? (pick<1, 4>(a, st))
                     : width <= 256  ? (pick<1, 8>(a, st))
                     : width <= 512  ? (pick<1, 16>(a, st))
@@ -423,11 +479,12 @@ int select_t(const SelectArgs& all, cudaStream_t st) {
 }  // namespace
 
 size_t select_key_bytes(const StoreArgs& st, int max_new) {
-  return static_cast<size_t>(st.n_seqs) * slab_tokens(st, max_new) * st.heads * st.width * 8;
+  return is_whole(st, max_new)
+             ? 0 : static_cast<size_t>(st.n_seqs) * slab_tokens(st, max_new) * st.heads * st.width * 8;
 }
 
 size_t select_sum_bytes(const StoreArgs& st, int max_new) {
-  return max_new < kStepTokens
+  return is_step(max_new)
              ? 0 : static_cast<size_t>(st.n_seqs) * slab_tokens(st, max_new) * st.heads * st.d * 8;
 }
 

@@ -140,6 +140,25 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// Launches clusters of `width` blocks along x.
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, unsigned width,
+                           cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = width;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 int launch_rotary(const uint16_t* x, int64_t x_stride, int64_t n, int heads, int d, int dtype,
                   const RotaryArgs& r, uint16_t* out, int64_t out_stride, cudaStream_t st);
 int launch_store_append(const StoreArgs& a, int dtype, const uint16_t* k, int64_t k_stride,

@@ -108,7 +108,7 @@ int attend_sizes(const fastnn_store* s, int64_t n, int heads_q, int max_new, int
 }
 
 size_t part_bytes(const AttendArgs& a) {
-  return a.splits > 1 ? static_cast<size_t>(a.splits) * a.n * a.hq * sizeof(float) : 0;
+  return a.splits > 1 && !a.pages ? static_cast<size_t>(a.splits) * a.n * a.hq * sizeof(float) : 0;
 }
 // Either kernel's partial outputs: which one runs also depends on the scale.
 size_t attend_bytes(const AttendArgs& a) {
@@ -179,10 +179,12 @@ int fastnn_attend(const fastnn_store* store, const void* q, int64_t q_stride, in
   FASTNN_TRY(row_checks(q, q_stride, static_cast<int64_t>(heads_q) * store->d));
   if (!store->k_pages || !aligned(store->k_pages, 16) || !store->v_pages ||
       !aligned(store->v_pages, 16) || !store->page_table || !store->lens || !store->cu || !out ||
-      !aligned(out, 16) || !aligned(lse, 4) || !workspace || !aligned(workspace, kAlign))
+      !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, kAlign))
     return FASTNN_ERR_INVALID;
   AttendArgs a = attend_args(store, n, heads_q, max_new, pages, select);
-  if (workspace_bytes < attend_bytes(a)) return FASTNN_ERR_CAPACITY;
+  const size_t need = attend_bytes(a);
+  if (!workspace && need > kAlign) return FASTNN_ERR_INVALID;
+  if (workspace && workspace_bytes < need) return FASTNN_ERR_CAPACITY;
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_stride;
   a.causal = causal ? 1 : 0;
@@ -203,7 +205,7 @@ size_t fastnn_select_workspace_size(const fastnn_store* store, int64_t n, int he
   if (attend_sizes(store, n, heads_q, max_new, 1) != FASTNN_OK) return 0;
   if (n == 0) return kAlign;
   const StoreArgs a = store_args(store);
-  return align_up(select_key_bytes(a, max_new)) + align_up(select_sum_bytes(a, max_new));
+  return kAlign + align_up(select_key_bytes(a, max_new)) + align_up(select_sum_bytes(a, max_new));
 }
 
 int fastnn_select_pages(const fastnn_store* store, const void* q, int64_t q_stride, int64_t n,
@@ -216,9 +218,11 @@ int fastnn_select_pages(const fastnn_store* store, const void* q, int64_t q_stri
   if (n == 0) return FASTNN_OK;
   FASTNN_TRY(row_checks(q, q_stride, static_cast<int64_t>(heads_q) * store->d));
   if (!store->k_mean || !aligned(store->k_mean, 16) || !store->page_table || !store->lens ||
-      !store->cu || !out_pages || !aligned(out_pages, 4) || !workspace || !aligned(workspace, kAlign))
+      !store->cu || !out_pages || !aligned(out_pages, 4) || !aligned(workspace, kAlign))
     return FASTNN_ERR_INVALID;
-  if (workspace_bytes < fastnn_select_workspace_size(store, n, heads_q, max_new)) return FASTNN_ERR_CAPACITY;
+  const size_t need = fastnn_select_workspace_size(store, n, heads_q, max_new);
+  if (!workspace && need > kAlign) return FASTNN_ERR_INVALID;
+  if (workspace && workspace_bytes < need) return FASTNN_ERR_CAPACITY;
   SelectArgs a{};
   a.st = store_args(store);
   a.q = static_cast<const uint16_t*>(q);
@@ -232,8 +236,8 @@ int fastnn_select_pages(const fastnn_store* store, const void* q, int64_t q_stri
   a.keep_last = keep_last;
   a.select = select;
   a.out = out_pages;
-  a.keys = static_cast<uint64_t*>(workspace);
-  a.sums = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) +
+  a.keys = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(workspace) + kAlign);
+  a.sums = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + kAlign +
                                      align_up(select_key_bytes(a.st, max_new)));
   return launch_select(a, store->dtype, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -100,7 +100,8 @@ def test_attend_refusals(lib):
     assert call(hq=3) == -1 and call(hq=0) == -1 and call(m=0) == -1 and call(m=6) == -1 and call(n=-2) == -1
     assert call(q=None) == -1 and call(q=FAKE + 4) == -1 and call(qs=200) == -1 and call(qs=260) == -1
     assert call(out=None) == -1 and call(out=FAKE + 8) == -1 and call(lse=FAKE + 2) == -1
-    assert call(ws=None) == -1 and call(ws=FAKE + 128) == -1 and call(nb=64) == -3
+    assert call(ws=FAKE + 128) == -1 and call(nb=64) == -3
+    assert call(_desc(table_width=4096), ws=None) == -1  # splits need their scratch
     assert call(scale=float("nan")) == -1 and call(scale=float("inf")) == -1
     assert call(pages=FAKE) == -1 and call(sel=4) == -1 and call(pages=FAKE, sel=-1) == -1
     for name in ("k_pages", "v_pages", "page_table", "lens", "cu"):
@@ -113,7 +114,8 @@ def test_select_refusals(lib):
     assert call(n=0, q=None, out=None, ws=None) == 0
     assert call(sel=0) == -1 and call(sel=257) == -1 and call(last=0) == -1 and call(first=-1) == -1
     assert call(first=4) == -1 and call(first=2, last=3) == -1 and call(hq=5) == -1
-    assert call(out=None) == -1 and call(q=None) == -1 and call(ws=None) == -1 and call(nb=0) == -3
+    assert call(out=None) == -1 and call(q=None) == -1 and call(nb=0) == -3
+    assert call(_desc(table_width=4097), ws=None) == -1
     assert call(_desc(k_mean=None)) == -1
     need = lib.fastnn_select_workspace_size(_desc(table_width=1 << 20), 5, 4, 3)  # a key of 8 bytes a page
     assert need >= 2 * 3 * 2 * (1 << 20) * 8 and call(_desc(table_width=1 << 20), nb=need - 1) == -3
