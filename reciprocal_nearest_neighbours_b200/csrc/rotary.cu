@@ -57,6 +57,27 @@ __device__ __forceinline__ void repack(const float (&f)[V], Pack<V>& p) {
   }
 }
 
+// i / n and i % n of i = start, start + stride, ...: a division at the start, an
+// addition and a carry a step (the append's loops are bound by
+// instructions, and an integer division takes some thirty of them).
+struct Split {
+  int q, r, n, dq, dr;
+  __device__ __forceinline__ Split(int start, int stride, int n_) : n(n_) {
+    q = start / n;
+    r = start - q * n;
+    dq = stride / n;
+    dr = stride - dq * n;
+  }
+  __device__ __forceinline__ void step() {
+    q += dq;
+    r += dr;
+    if (r >= n) {
+      r -= n;
+      ++q;
+    }
+  }
+};
+
 __device__ __forceinline__ float2 turn_of(const RotaryArgs& r, int pos, int j) {
   double t = static_cast<double>(pos) * (__ldg(r.freq + j) * kTurnsPerRadian);
   t -= rint(t);
@@ -189,31 +210,39 @@ append_kernel(StoreArgs st, const uint16_t* k, int64_t k_stride, const uint16_t*
   const uint16_t* vs = v + tok0 * v_stride + static_cast<int64_t>(h) * st.dv;
   const int rows = fill - first;
 
+  // The page's rows of one head lie one after the other.
   const int vc = st.dv / 8;
-  for (int i = tid; i < rows * vc; i += kAppendThreads) {
-    const int row = i / vc, c = i - row * vc;
-    reinterpret_cast<uint4*>(vp + static_cast<int64_t>(first + row) * st.dv)[c] =
-        __ldg(reinterpret_cast<const uint4*>(vs + row * v_stride) + c);
-  }
+  uint4* v_out = reinterpret_cast<uint4*>(vp + static_cast<int64_t>(first) * st.dv);
+  Split at_v(tid, kAppendThreads, vc);
+#pragma unroll 4
+  for (int i = tid; i < rows * vc; i += kAppendThreads, at_v.step())
+    v_out[i] = __ldg(reinterpret_cast<const uint4*>(vs + at_v.q * v_stride) + at_v.r);
   const int nt = r.rot ? r.axes * r.nf : 0;
   const int items = nt / V, rest = (st.d - r.rot) / V;
   for (int b = 0; b < rows; b += kAppendRows) {
     const int m = rows - b < kAppendRows ? rows - b : kAppendRows;
     if (b) __syncthreads();
-    for (int i = tid; i < m * nt; i += kAppendThreads) {
-      const int t = i / nt, j = i - t * nt, a = j >= r.nf ? 1 : 0;
-      turns[i] = turn_of(r, __ldg(r.pos + (tok0 + b + t) * r.axes + a), j - a * r.nf);
+    if (nt) {
+      Split at(tid, kAppendThreads, nt);
+      for (int i = tid; i < m * nt; i += kAppendThreads, at.step()) {
+        const int a = at.r >= r.nf ? 1 : 0;
+        turns[i] = turn_of(r, __ldg(r.pos + (tok0 + b + at.q) * r.axes + a), at.r - a * r.nf);
+      }
     }
     __syncthreads();
-    for (int i = tid; i < m * items; i += kAppendThreads) {
-      const int t = i / items;
-      rotate_item<T, V>(ks + (b + t) * k_stride, kp + static_cast<int64_t>(first + b + t) * st.d,
-                        i - t * items, turns + t * nt, r);
+    if (nt) {
+      Split at(tid, kAppendThreads, items);
+      for (int i = tid; i < m * items; i += kAppendThreads, at.step())
+        rotate_item<T, V>(ks + (b + at.q) * k_stride, kp + (first + b + at.q) * st.d, at.r, turns + at.q * nt, r);
     }
-    for (int i = tid; i < m * rest; i += kAppendThreads) {
-      const int t = i / rest, e = r.rot + (i - t * rest) * V;
-      *reinterpret_cast<typename Vec<V>::type*>(kp + static_cast<int64_t>(first + b + t) * st.d + e) =
-          *reinterpret_cast<const typename Vec<V>::type*>(ks + (b + t) * k_stride + e);
+    if (rest) {
+      Split at(tid, kAppendThreads, rest);
+#pragma unroll 4
+      for (int i = tid; i < m * rest; i += kAppendThreads, at.step()) {
+        const int e = r.rot + at.r * V;
+        *reinterpret_cast<typename Vec<V>::type*>(kp + (first + b + at.q) * st.d + e) =
+            __ldg(reinterpret_cast<const typename Vec<V>::type*>(ks + (b + at.q) * k_stride + e));
+      }
     }
   }
   if (!st.mean) return;
