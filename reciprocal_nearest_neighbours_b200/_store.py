@@ -40,6 +40,10 @@ _STATUS = 256  # bytes of a workspace that holds nothing but the status word
 
 _bound = None
 _I32 = torch.int32
+# What torch.cuda.current_stream and current_device come down to, without their wrapping (3 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _lib():
@@ -108,13 +112,13 @@ def _launch(what: str, dev: int, stream, *args):
     """Call the library with the tensors' device current, on ``stream`` (None: the device's
     current one)."""
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
+        raw = _raw_stream(dev)
     else:
         if stream.device.index != dev:
             raise ValueError(f"the stream is on {stream.device}, the tokens on cuda:{dev}")
         raw = stream.cuda_stream
     fn = getattr(_bound, what)
-    if torch._C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -146,22 +150,23 @@ def _pages(k_pages, v_pages, dev, dtype):
     return shape, other[3], kp, vp
 
 
-def _new(shape, dtype, dev, stream):
-    """A tensor that a launch on ``stream`` (None: the current one) writes: on another stream
-    than the one it was allocated on, its memory must not go round before that launch is done."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
+def _new(like, shape, dtype, stream):
+    """A tensor on the device of ``like`` that a launch on ``stream`` (None: the current one)
+    writes: on another stream than the one it was allocated on, its memory must not go round
+    before that launch is done."""
+    t = like.new_empty(shape, dtype=dtype)
     if stream is not None:
         t.record_stream(stream)
     return t
 
 
-def _scratch(need: int, dev, workspace, what: str, stream) -> int:
+def _scratch(need: int, like, dev, workspace, what: str, stream) -> int:
     """Address of the call's workspace, 0 for none: _STATUS bytes hold no more than the status
     word, which nobody reads where the caller brings no workspace."""
     if need == 0:
         raise FastNNError(-1, what)
     if workspace is None:
-        return 0 if need == _STATUS else _new(need, torch.uint8, dev, stream).data_ptr()
+        return 0 if need == _STATUS else _new(like, need, torch.uint8, stream).data_ptr()
     if workspace.get_device() != dev:
         raise ValueError(f"the workspace is on {workspace.device}, the tokens on cuda:{dev}")
     if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
@@ -219,7 +224,7 @@ def fastnn_rotary(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, layout
     xs = _rows(x, "x", n, heads, d)
     rot = _rotation(pos, freq, layout, scale, n, dev)
     if out is None:
-        out = _new((n, heads, d), x.dtype, dev, stream)
+        out = _new(x, (n, heads, d), x.dtype, stream)
         to, os = out.data_ptr(), heads * d
     else:
         to, os = _same(dev, x.dtype, "out", out), _rows(out, "out", n, heads, d)
@@ -258,7 +263,7 @@ def fastnn_store_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
     rot = None if pos is None else _rotation(pos, freq, layout, scale, n, dev)
     ws = None
     if workspace is not None:
-        ws = _scratch(FASTNN_STORE_APPEND_WORKSPACE, dev, workspace, "", stream)
+        ws = _scratch(FASTNN_STORE_APPEND_WORKSPACE, k, dev, workspace, "", stream)
     _bound or _lib()
     _launch("fastnn_store_append", dev, stream, store, k.data_ptr(), ks, at_v, vs, n, max_new, rot,
             ws, FASTNN_STORE_APPEND_WORKSPACE)
@@ -302,19 +307,19 @@ def fastnn_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
             raise ValueError(f"pages must be [{n}, {heads}, select], got {tuple(pages.shape)}")
         select = pages.shape[2]
     if out is None:
-        out = _new((n, hq, dv), dtype, dev, stream)
+        out = _new(q, (n, hq, dv), dtype, stream)
     else:
         _same(dev, dtype, "out", out)
         if out.shape != (n, hq, dv) or not out.is_contiguous():
             raise ValueError(f"out must be contiguous [{n}, {hq}, {dv}]")
     if lse is None:
-        lse = _new((n, hq), torch.float32, dev, stream)
+        lse = _new(q, (n, hq), torch.float32, stream)
     else:
         _same(dev, torch.float32, "lse", lse)
         if lse.shape != (n, hq) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous [{n}, {hq}]")
     need = (_bound or _lib()).fastnn_attend_workspace_size(store, n, hq, max_new, select)
-    ws = _scratch(need, dev, workspace, "fastnn_attend_workspace_size", stream)
+    ws = _scratch(need, q, dev, workspace, "fastnn_attend_workspace_size", stream)
     _launch("fastnn_attend", dev, stream, store, q.data_ptr(), qs, n, hq, max_new, causal,
             d ** -0.5 if scale is None else scale, listed, select, out.data_ptr(), lse.data_ptr(),
             ws, need)
@@ -344,13 +349,13 @@ def fastnn_select_pages(q: torch.Tensor, k_mean: torch.Tensor, page_table: torch
     qs = _rows(q, "q", n, hq, d)
     store = _describe(code, dev, page_table, lens, cu, n_pages, heads, page, d, 8, None, None, mean)
     if out is None:
-        out = _new((n, heads, select), _I32, dev, stream)
+        out = _new(q, (n, heads, select), _I32, stream)
     else:
         _index(out, "out", 3, dev)
         if out.shape != (n, heads, select):
             raise ValueError(f"out must be [{n}, {heads}, {select}]")
     need = (_bound or _lib()).fastnn_select_workspace_size(store, n, hq, max_new)
-    ws = _scratch(need, dev, workspace, "fastnn_select_workspace_size", stream)
+    ws = _scratch(need, q, dev, workspace, "fastnn_select_workspace_size", stream)
     _launch("fastnn_select_pages", dev, stream, store, q.data_ptr(), qs, n, hq, max_new, causal,
             keep_first, keep_last, select, out.data_ptr(), ws, need)
     return out

@@ -586,8 +586,7 @@ int rows_launch(const AttendArgs& a, cudaStream_t st) {
   using D = Depth<DP, MANY>;
   using S = RowsSmem<DP, NT, D::kStages>;
   static_assert(D::kBlocks * (S::kTotal + 1024) <= 228 * 1024, "the blocks fit an SM");
-  FASTNN_CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<T, DP, NT, SEL, FULL, MANY>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal));
+  FASTNN_CUDA_TRY((allow_smem<attend_rows_kernel<T, DP, NT, SEL, FULL, MANY>>(S::kTotal)));
   const int64_t tiles = row_tiles(a);
   if (tiles * a.splits > INT32_MAX) return FASTNN_ERR_INVALID;
   const dim3 grid(static_cast<unsigned>(tiles * a.splits), a.st.heads, a.st.n_seqs);

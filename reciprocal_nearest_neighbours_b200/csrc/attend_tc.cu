@@ -1014,8 +1014,7 @@ int tc_launch(const AttendArgs& all, cudaStream_t stream) {
                  static_cast<uint64_t>(st.page) * st.dv, st.page, 1);
   if (e != FASTNN_OK) return e;
   FASTNN_CUDA_TRY(cudaMemsetAsync(all.status, 0, sizeof(int), stream));
-  FASTNN_CUDA_TRY(cudaFuncSetAttribute(attend_tc_kernel<T, DP>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+  FASTNN_CUDA_TRY((allow_smem<attend_tc_kernel<T, DP>>(kSmem)));
   for (int s0 = 0; s0 < st.n_seqs; s0 += kMaxSeqs) {
     TcArgs q = p;
     q.a.st.n_seqs = st.n_seqs - s0 < kMaxSeqs ? st.n_seqs - s0 : kMaxSeqs;

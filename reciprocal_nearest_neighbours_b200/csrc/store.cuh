@@ -2,6 +2,7 @@
 // 16-bit float conversions). Entry points: store_api.cu.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -123,6 +124,22 @@ struct Half16<__half> {
     return r;
   }
 };
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device; the
+// attribute is set once a device (setting it takes as long as a small launch's
+// other host work).
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Launches a kernel that starts with cudaGridDependencySynchronize(): its
 // blocks may be brought up while the stream's previous kernel drains.
