@@ -97,6 +97,12 @@ __device__ __forceinline__ int seg_visible(const Seg& e, int i) {
   return v < 0 ? 0 : v < e.cap ? static_cast<int>(v) : e.cap;
 }
 
+// Where the loading warp stands at its end.
+struct Loads {
+  int stage, phase, fix_phase, segs;
+  uint32_t open;  // stages that it has loaded; bit 31: a load on `fix` is under way
+};
+
 struct TcCtl {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
@@ -107,6 +113,7 @@ struct TcCtl {
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];
   Seg seg[kSegRing];
   uint32_t holes[kHoleRing];
+  Loads loads;
   uint32_t tmem;
   int abort;
 };
@@ -349,13 +356,19 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t block)
          (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Inlined: a call would have to be possible within either register share.
-__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, TcCtl* ctl, int* status,
-                                       uint64_t limit) {
+// Bounded wait for a phase; false, with the abort flag and the status set, if
+// `limit` ns pass or another role has given up. A suspended test may take
+// longer than a short limit, so such limits are watched by polling. (Inlined: a
+// call would have to be possible within either register share.)
+constexpr uint64_t kPolledLimit = 10000000;
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, TcCtl* ctl, int* status,
+                                         uint64_t limit) {
+  const bool polled = limit < kPolledLimit;
+  if (polled ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   for (uint32_t n = 1;; ++n) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    if ((n & 63) == 0 || n == 8) {
+    if (polled ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+    if (polled || (n & 63) == 0 || n == 8) {
       if (*reinterpret_cast<volatile int*>(&ctl->abort)) return false;
       if (ptx::globaltimer_ns() - t0 > limit) {
         *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
@@ -364,11 +377,6 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, TcCtl* 
       }
     }
   }
-}
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, TcCtl* ctl, int* status,
-                                         uint64_t limit) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, ctl, status, limit);
 }
 
 // ---- the kernel -----------------------------------------------------------------
@@ -622,7 +630,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       uint32_t phase = 0, fix_phase = 0, q_phase = 0;
       int tiles = 0, segs = 0;
       const int nkb = (st.d + 63) / 64, nvb = (st.dv + 63) / 64;
-      uint32_t open_stages = 0;  // stages with a load in flight when the role gives up
+      uint32_t open_stages = 0;  // see Loads
       bool ok = true;
       Seg e;
       while (segment(segs, e)) {
@@ -704,26 +712,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         }
         if (!ok) break;
       }
-      if (*reinterpret_cast<volatile int*>(&ctl->abort)) {
-        // Copies that nobody will wait for any more: wait for their bytes (the
-        // limit is the default one). A stage's last load completes the phase
-        // that follows its last wait on `empty`.
-        for (int i = 0; i < C::kStages; ++i) {
-          if (!((open_stages >> i) & 1u)) continue;
-          const uint32_t par = i < stage ? phase : phase ^ 1u;
-          const uint64_t t0 = ptx::globaltimer_ns();
-          while (!ptx::mbar_test_wait(bar(ctl->full[i]), par) && ptx::globaltimer_ns() - t0 < kTimeoutNs) {
-          }
-        }
-        const uint64_t t0 = ptx::globaltimer_ns();
-        if (open_stages >> 31)
-          while (!ptx::mbar_test_wait(bar(ctl->fix), fix_phase) && ptx::globaltimer_ns() - t0 < kTimeoutNs) {
-          }
-        if (segs > 0)
-          while (!ptx::mbar_test_wait(bar(ctl->q_full), (segs - 1) & 1) &&
-                 ptx::globaltimer_ns() - t0 < kTimeoutNs) {
-          }
-      }
+      if (lane == 0) ctl->loads = Loads{stage, static_cast<int>(phase), static_cast<int>(fix_phase), segs, open_stages};
     } else if (warp == kMmaWarp) {
       // The whole warp waits; one elected lane issues.
       const bool leader = elect_one();
@@ -874,6 +863,22 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  if (tid == 0 && ctl->abort) {
+    // Some role has given up, and copies may be under way that nobody waits for
+    // any more: the block stays until their bytes are there (within the default
+    // limit). A stage's last load completes the phase after its last wait on `empty`.
+    const Loads d = ctl->loads;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    auto drain = [&](uint64_t& b, uint32_t parity) {
+      while (!ptx::mbar_test_wait(bar(b), parity) && ptx::globaltimer_ns() - t0 < kTimeoutNs) {
+      }
+    };
+    for (int i = 0; i < C::kStages; ++i)
+      if ((d.open >> i) & 1u) drain(ctl->full[i], static_cast<uint32_t>(i < d.stage ? d.phase : d.phase ^ 1));
+    if (d.open >> 31) drain(ctl->fix, static_cast<uint32_t>(d.fix_phase));
+    if (d.segs > 0) drain(ctl->q_full, static_cast<uint32_t>((d.segs - 1) & 1));
+  }
+  __syncthreads();
   if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
 }
 

@@ -502,6 +502,65 @@ def test_captured_step_follows_the_store(news):
             ref.check_attend(x.sparse[0], x.sparse[1], have, pages=want)
 
 
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    """The tensor-core kernel's bounded waits, with a limit far below the call's duration: the call
+    ends, its status says so, and the next one on the same workspace is right."""
+    st = ref.Store([300, 0], [140, 200], 64, 2, 64, 64, BF16, seed=31, group=2)
+    q, kp, vp, table, lens, cu = st.cuda("q", "k_pages", "v_pages", "table", "lens", "cu")
+    need = fnn.fastnn_attend_workspace_size(st.n, 4, 2, 64, 64, 2, st.max_new, st.width, 64)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    fnn.fastnn_set_wait_timeout_ns(200)
+    try:
+        fnn.fastnn_attend(q, kp, vp, table, lens, cu, st.max_new, workspace=ws)
+        assert fnn.fastnn_device_status(ws) == -5
+    finally:
+        fnn.fastnn_set_wait_timeout_ns(0)
+    out, lse = fnn.fastnn_attend(q, kp, vp, table, lens, cu, st.max_new, workspace=ws)
+    assert fnn.fastnn_device_status(ws) == 0
+    ref.check_attend(out, lse, st)
+
+
+@pytest.mark.parametrize("news", [[1, 1], [90, 200]])
+def test_queries_as_part_of_a_fused_projection(news):
+    st = ref.Store([77, 5], news, 32, 2, 64, 64, F16, seed=32, group=2)
+    fused = torch.zeros(st.n, 8, 64, dtype=F16, device="cuda")
+    fused[:, 2:6] = st.q.cuda()
+    fused[:, :2] = fused[:, 6:] = float("nan")
+    kp, vp, km, table, lens, cu = st.cuda("k_pages", "v_pages", "k_mean", "table", "lens", "cu")
+    out, lse = fnn.fastnn_attend(fused[:, 2:6], kp, vp, table, lens, cu, st.max_new)
+    ref.check_attend(out, lse, st)
+    pages = fnn.fastnn_select_pages(fused[:, 2:6], km, table, lens, cu, st.max_new, 32, 3)
+    assert torch.equal(pages.cpu(), ref.select_pages(st, st.k_mean, 3, 0, 1))
+    again = fnn.fastnn_attend(fused[:, 2:6], kp, vp, table, lens, cu, st.max_new)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])  # the same bits
+
+
+def test_many_sequences_at_once():
+    """More sequences than one launch of the tensor-core kernel plans for, most without a token."""
+    seqs = 700
+    news = [(70 if s % 101 == 0 else 0) for s in range(seqs)]
+    lens = [s % 50 for s in range(seqs)]
+    st = ref.Store(lens, news, 16, 1, 16, 16, BF16, seed=33)
+    out, lse = _attend(st)
+    ref.check_attend(out, lse, st)
+    one = ref.Store(lens, [1] * seqs, 16, 1, 16, 16, BF16, seed=34)
+    out, lse = _attend(one)
+    ref.check_attend(out, lse, one)
+    q, km, table, ln, cu = one.cuda("q", "k_mean", "table", "lens", "cu")
+    got = fnn.fastnn_select_pages(q, km, table, ln, cu, 1, 16, 2)
+    assert torch.equal(got.cpu(), ref.select_pages(one, one.k_mean, 2, 0, 1))
+
+
+def test_select_over_many_pages():
+    """Tables wider than a block's registers (4096 pages), and between the kernels' borders."""
+    for width, news, dtype in ((4200, [1], BF16), (4200, [9], F16), (1100, [3], BF16), (513, [12], F16),
+                               (512, [7], BF16)):
+        st = ref.Store([width * 16 - 40], news, 16, 1, 16, 16, dtype, seed=width, group=2)
+        q, km, table, ln, cu = st.cuda("q", "k_mean", "table", "lens", "cu")
+        got = fnn.fastnn_select_pages(q, km, table, ln, cu, news[0], 16, 200, keep_first=2, keep_last=3)
+        assert torch.equal(got.cpu(), ref.select_pages(st, st.k_mean, 200, 2, 3)), width
+
+
 def test_another_stream_than_the_current_one():
     st = ref.Store([500], [30], 16, 1, 64, 64, F16, seed=22, group=2)
     q, kp, vp, table, lens, cu = st.cuda("q", "k_pages", "v_pages", "table", "lens", "cu")
