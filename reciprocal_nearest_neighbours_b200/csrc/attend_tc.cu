@@ -68,16 +68,18 @@ struct Tc {
   static constexpr int kCtl = kRing + kStages * kTile;
   static constexpr int kBlock = kBlk * 128;        // bytes of a 64-element column block
   // Of every 16 pairs of weights, so many by polynomial (12 instructions a pair
-  // against 16 clocks of the special-function unit): where the products are
-  // short, the softmax is what takes the time. Measured with 0 / 2 / 5: 12288
-  // queries over 196608 keys of 24 876 / 805 / 785 us; 2048 over 16384, 32 heads of
-  // 128, 434 / 425 / 432 us.
-  static constexpr int kPolyPairs = DP == 128 ? 2 : 5;
+  // against 16 clocks of the special-function unit). Measured with 2 / 5 / 7:
+  // 12288 queries over 196608 keys of 24 765 / 800 / 822 us; with 0 / 2 / 5: 2048
+  // over 16384, 32 heads of 128, 434 / 425 / 432 us.
+  static constexpr int kPolyPairs = 2;
+  // Tensor memory columns of query tile w: scores at 128 w, O at kO + DP w, the
+  // weights (packed in pairs, 64 columns) at kP + kPStep w: over the scores where
+  // all 512 columns are in use (DP = 128), else by themselves, so that the
+  // next scores need not wait for the weights' product.
+  static constexpr bool kOwnP = DP == 64;
+  static constexpr uint32_t kO = 256, kP = kOwnP ? 384 : 0, kPStep = kOwnP ? 64 : 128;
 };
 
-// Tensor memory columns of query tile w: scores at 128 w, the weights over
-// them (packed in pairs, 64 columns), O at 256 + 128 w.
-constexpr uint32_t kOCol = 256;
 
 constexpr int kMaxStages = 8;
 constexpr int kSegRing = 4;        // segments the planning warp is ahead of the others
@@ -108,8 +110,9 @@ struct TcCtl {
   uint64_t empty[kMaxStages];
   uint64_t q_full, q_empty, fix, done;
   uint64_t s_full[2];   // scores are there
+  uint64_t s_free[2];   // kOwnP: the scores have been read
   uint64_t p_full[2];   // the weights are there
-  uint64_t o_full[2];   // a segment's last product is complete
+  uint64_t pv_done[2];  // a tile's second product is complete (!kOwnP: a segment's last)
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];
   Seg seg[kSegRing];
   uint32_t holes[kHoleRing];
@@ -408,7 +411,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     for (int w = 0; w < 2; ++w) {
       ptx::mbar_init(bar(ctl->s_full[w]), 1);
       ptx::mbar_init(bar(ctl->p_full[w]), 4);
-      ptx::mbar_init(bar(ctl->o_full[w]), 1);
+      ptx::mbar_init(bar(ctl->s_free[w]), 4);
+      ptx::mbar_init(bar(ctl->pv_done[w]), 1);
     }
     for (int i = 0; i < kSegRing; ++i) {
       ptx::mbar_init(bar(ctl->seg_full[i]), 1);
@@ -466,10 +470,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int w = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + kOCol + w * 128;
+    const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + C::kO + w * DP;
+    const uint32_t tp = tmem + lanes + C::kP + w * C::kPStep;
     const int nvb = (st.dv + 63) / 64;
     const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
-    uint32_t sp = 0, op = 0;  // parities of s_full and o_full
+    uint32_t sp = 0, pd = 1;  // parities: of s_full, and of pv_done's last completed phase
     int tiles = 0;
     Seg e;
     for (int k = 0; segment(k, e); ++k) {
@@ -562,6 +567,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             l *= f;
             m = up;
             if (t > 0) {
+              if (C::kOwnP)
+                ok = __all_sync(0xffffffffu, wait_for(bar(ctl->pv_done[w]), pd, ctl, a.status, limit));
+              ptx::tc_fence_after();
               for (int c = 0; c < nvb * 2; ++c) {
                 uint32_t o[32];
                 ptx::tmem_ld32(to + c * 32, o);
@@ -575,16 +583,27 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           sum = weigh(std::integral_constant<int, 0>{});
         }
         l += sum;
+        if (C::kOwnP) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(ctl->s_free[w]));
+          if (t > 0) {  // the weights before these have been used
+            ok = ok && __all_sync(0xffffffffu, wait_for(bar(ctl->pv_done[w]), pd, ctl, a.status, limit));
+            ptx::tc_fence_after();
+          }
+          if (!ok) break;
+        }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_st16(ts + c * 16, pk[c]);
+        for (int c = 0; c < 4; ++c) tmem_st16(tp + c * 16, pk[c]);
         tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(ctl->p_full[w]));
+        if (C::kOwnP) pd ^= 1;
       }
       if (!ok) break;
-      ok = __all_sync(0xffffffffu, wait_for(bar(ctl->o_full[w]), op, ctl, a.status, limit));
-      op ^= 1;
+      if (!C::kOwnP) pd ^= 1;
+      ok = __all_sync(0xffffffffu, wait_for(bar(ctl->pv_done[w]), pd, ctl, a.status, limit));
       if (!ok) break;
       ptx::tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
@@ -724,7 +743,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       const int ksteps = (st.d + 15) / 16;
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t pp = 0;  // bit w: the parity that p_full[w] completes next
+      uint32_t pp = 0;  // bit w: the parity that p_full[w] (and s_free[w]) completes next
       auto await = [&](uint64_t& b, uint32_t parity) {
         return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, a.status, limit));
       };
@@ -743,7 +762,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         const uint64_t vd = smem_desc_mn(sbase + C::kRing + vstage * C::kTile, C::kBlock);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tmem + kOCol + w * 128, tmem + w * 128 + ks * 8, vd + ks * (2048 >> 4), idesc_o,
+          mma_ts(tmem + C::kO + w * DP, tmem + C::kP + w * C::kPStep + ks * 8, vd + ks * (2048 >> 4), idesc_o,
                  (fresh && ks == 0) ? 0u : 1u);
       };
       auto step = [&]() {
@@ -771,16 +790,18 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           const bool more = t + 1 < nt;
           if (more && !(ok = await(ctl->full[stage], phase))) break;
           for (int w = 0; w < nw; ++w) {
+            if (C::kOwnP) {
+              if (!(ok = await(ctl->s_free[w], (pp >> w) & 1u))) break;
+              ptx::tc_fence_after();
+              if (leader && more) product_s(w, stage);
+            }
             if (!(ok = await(ctl->p_full[w], (pp >> w) & 1u))) break;
             pp ^= 1u << w;
             ptx::tc_fence_after();
             if (leader) {
               product_o(w, vstage, t == 0);
-              if (more) {
-                product_s(w, stage);
-              } else {
-                ptx::mma_commit(bar(ctl->o_full[w]));
-              }
+              if (C::kOwnP || !more) ptx::mma_commit(bar(ctl->pv_done[w]));
+              if (!C::kOwnP && more) product_s(w, stage);
             }
           }
           if (!ok) break;
