@@ -520,53 +520,66 @@ attend_rows_kernel(AttendArgs a) {
   }
 }
 
-// Joins the splits of each row: out = sum_i 2^(lse2_i - lse2) out_i. A warp
-// takes one row.
+// Joins the splits of a row: out = sum_i 2^(lse2_i - lse2) out_i. A block takes one
+// row, its warps every fourth split each (a warp alone would wait for some tens
+// of them one after the other: 3 long sequences 119 us against 106).
 template <typename T>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kThreads)
 combine_kernel(AttendArgs a) {
   cudaGridDependencySynchronize();
+  __shared__ float tops[kWarps], sums[kWarps];
+  __shared__ float4 parts_v[kWarps][32];
   const StoreArgs& st = a.st;
-  const int s = blockIdx.y, lane = threadIdx.x & 31;
+  const int s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const SeqView w = seq_view(st, s, a.n, a.max_new, a.causal);
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int64_t r = blockIdx.x;
   if (r >= static_cast<int64_t>(w.n) * a.hq) return;
-  const int tok = static_cast<int>(r / a.hq);
-  const int vis = visible(w, tok);
+  const int vis = visible(w, static_cast<int>(r / a.hq));
   const int parts = (vis + a.split_len - 1) / a.split_len;
   if (parts <= 1) return;  // its one split has written the result
   const int64_t row = static_cast<int64_t>(w.t0) * a.hq + r;
   const int64_t step = a.n * a.hq;
   float top = -INFINITY;
-  for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_lse[i * step + row]);
+  for (int i = threadIdx.x; i < parts; i += kThreads) top = fmaxf(top, a.part_lse[i * step + row]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kWarps; ++q) top = fmaxf(top, tops[q]);
+  const bool any = top > -INFINITY;
   float sum = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   const int c = lane * 4;
-  if (top > -INFINITY) {
-    for (int i = 0; i < parts; ++i) {
-      const float f = ex2(a.part_lse[i * step + row] - top);
-      sum += f;
-      if (c < st.dv) {
-        const float4 y = *reinterpret_cast<const float4*>(a.part + (i * step + row) * st.dv + c);
-        v.x += f * y.x;
-        v.y += f * y.y;
-        v.z += f * y.z;
-        v.w += f * y.w;
-      }
-    }
-    const float inv = 1.f / sum;
-    v.x *= inv;
-    v.y *= inv;
-    v.z *= inv;
-    v.w *= inv;
+#pragma unroll 4
+  for (int i = warp; i < parts; i += kWarps) {
+    const float f = any ? ex2(a.part_lse[i * step + row] - top) : 0.f;
+    const float4 y = c < st.dv ? *reinterpret_cast<const float4*>(a.part + (i * step + row) * st.dv + c)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+    sum += f;
+    v.x += f * y.x;
+    v.y += f * y.y;
+    v.z += f * y.z;
+    v.w += f * y.w;
   }
+  parts_v[warp][lane] = v;
+  if (lane == 0) sums[warp] = sum;
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll
+  for (int q = 1; q < kWarps; ++q) {
+    const float4 y = parts_v[q][lane];
+    sum += sums[q];
+    v.x += y.x;
+    v.y += y.y;
+    v.z += y.z;
+    v.w += y.w;
+  }
+  const float inv = any ? 1.f / sum : 0.f;
   if (c < st.dv)
     *reinterpret_cast<uint2*>(a.out + row * st.dv + c) =
-        make_uint2(Half16<T>::pack(v.x, v.y), Half16<T>::pack(v.z, v.w));
-  if (lane == 0 && a.lse)
-    a.lse[row] = top > -INFINITY ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+        make_uint2(Half16<T>::pack(v.x * inv, v.y * inv), Half16<T>::pack(v.z * inv, v.w * inv));
+  if (lane == 0 && a.lse) a.lse[row] = any ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
 // Groups of 8 query rows of a block: one if no block would have more rows.
@@ -598,9 +611,10 @@ int rows_launch(const AttendArgs& a, cudaStream_t st) {
   attend_rows_kernel<T, DP, NT, SEL, FULL, MANY><<<grid, kThreads, S::kTotal, st>>>(a);
   FASTNN_CUDA_TRY(cudaGetLastError());
   if (a.splits > 1) {
-    const int64_t blocks = (static_cast<int64_t>(a.max_new) * a.hq + 3) / 4;
-    FASTNN_CUDA_TRY(launch_after(combine_kernel<T>, dim3(static_cast<unsigned>(blocks), a.st.n_seqs),
-                                 dim3(128), st, a));
+    const int64_t rows = static_cast<int64_t>(a.max_new) * a.hq;  // few: there are fewer tiles than blocks wanted
+    if (rows > INT32_MAX) return FASTNN_ERR_INVALID;
+    FASTNN_CUDA_TRY(launch_after(combine_kernel<T>, dim3(static_cast<unsigned>(rows), a.st.n_seqs),
+                                 dim3(kThreads), st, a));
   }
   return FASTNN_OK;
 }
