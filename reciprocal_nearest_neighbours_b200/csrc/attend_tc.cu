@@ -905,7 +905,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 
 // Joins the partial outputs of the items that a share's border divides. Block
 // (c, i) looks at the border before CTA c + 1 and takes every gridDim.y-th group
-// of rows of its item, if the item's first cut is there.
+// of rows of its item, if the item's first cut is there. A warp takes a row; its
+// lanes look at the CTAs c, c + 1, ... that may have a part, 32 at a time.
 template <typename T>
 __global__ void __launch_bounds__(256)
 merge_kernel(const __grid_constant__ TcArgs p) {
@@ -913,27 +914,30 @@ merge_kernel(const __grid_constant__ TcArgs p) {
   const AttendArgs& a = p.a;
   const StoreArgs& st = a.st;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x + 1, ctas = p.ctas;
-  __shared__ Cut cuts[kMaxCtas];
-  const Cut sp = p.cuts[c];
-  if (sp.u0 >= sp.u1 || sp.u0 == sp.base || p.cuts[c - 1].u0 > sp.base) return;
-  for (int i = threadIdx.x; i < ctas * static_cast<int>(sizeof(Cut) / 16); i += 256)
-    reinterpret_cast<int4*>(cuts)[i] = reinterpret_cast<const int4*>(p.cuts)[i];
-  __syncthreads();
-  const int64_t base = sp.base, end = sp.end;
-  // The CTAs c - 1 .. last have a part each, but for those without a tile.
-  auto has_part = [&](const Cut& k) {
-    return tiles_of((k.u1 < end ? k.u1 : end) - base) > tiles_of(k.u0 > base ? k.u0 - base : 0);
-  };
-  int parts = 0, last = c - 1;
-  for (int k = c - 1; k < ctas; ++k) {
-    const Cut& cut = cuts[k];
-    if (cut.u0 >= end || cut.u0 >= cut.u1) break;
-    parts += has_part(cut);
-    last = k;
-  }
-  if (parts <= 1) return;
+  const int c = blockIdx.x;
+  const Cut sp = p.cuts[c + 1];
+  if (sp.u0 >= sp.u1 || sp.u0 == sp.base || p.cuts[c].u0 > sp.base) return;
   const SeqView w = seq_view(st, sp.s, a.n, a.max_new, a.causal);
+  const int64_t base = sp.base, end = sp.end;
+  // Lane's slot of partial outputs among CTAs k0 .. k0 + 31, -1: none.
+  auto slot_of = [&](int k0) {
+    const int k = k0 + lane;
+    if (k >= p.ctas) return -1;
+    const Cut cut = p.cuts[k];
+    const bool part = cut.u0 < end && cut.u0 < cut.u1 &&
+                      tiles_of((cut.u1 < end ? cut.u1 : end) - base) > tiles_of(cut.u0 > base ? cut.u0 - base : 0);
+    return part ? 2 * k + (cut.u0 < base ? 1 : 0) : -1;
+  };
+  int windows = 0, parts = 0;
+  const int first = slot_of(c);
+  for (int k0 = c; k0 < p.ctas; k0 += 32) {
+    const int found = __popc(__ballot_sync(0xffffffffu, (k0 == c ? first : slot_of(k0)) >= 0));
+    if (found) {
+      parts += found;
+      windows = (k0 - c) / 32 + 1;
+    }
+  }
+  if (parts <= 1) return;  // one CTA had all its tiles
   const int i0 = sp.tile * 2 * p.tt;
   for (int rr = blockIdx.y * 8 + warp; rr < 256; rr += gridDim.y * 8) {
     const int q = rr >> 7, r = rr & 127;
@@ -942,26 +946,35 @@ merge_kernel(const __grid_constant__ TcArgs p) {
     const int64_t row = (static_cast<int64_t>(w.t0) + tok) * a.hq + sp.g * a.group + r % a.group;
     float top = -INFINITY, sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int pass = 0; pass < 2; ++pass) {
-      for (int k = c - 1; k <= last; ++k) {
-        const Cut& cut = cuts[k];
-        if (!has_part(cut)) continue;
-        const int slot = 2 * k + (cut.u0 < base ? 1 : 0);
-        const float z = p.part_lse[slot * 256 + rr];
-        if (pass == 0) {
-          top = fmaxf(top, z);
-          continue;
-        }
-        if (top == -INFINITY) continue;
-        const float f = ex2(z - top);
-        sum += f;
+    for (int x = 0; x < windows; ++x) {
+      const int slot = x == 0 ? first : slot_of(c + 32 * x);
+      const float z = slot >= 0 ? p.part_lse[slot * 256 + rr] : -INFINITY;
+      float up = fmaxf(top, z);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+      if (up == -INFINITY) continue;
+      const float old = top == -INFINITY ? 0.f : ex2(top - up);
+      sum *= old;
+      v.x *= old;
+      v.y *= old;
+      v.z *= old;
+      v.w *= old;
+      top = up;
+      const float f = slot >= 0 ? ex2(z - up) : 0.f;
+      unsigned some = __ballot_sync(0xffffffffu, slot >= 0);
+      while (some) {
+        const int k = __ffs(some) - 1;
+        some &= some - 1;
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        const int sk = __shfl_sync(0xffffffffu, slot, k);
+        sum += fk;
         if (lane * 4 < st.dv) {
           const float4 y = *reinterpret_cast<const float4*>(
-              p.part + (static_cast<int64_t>(slot) * 256 + rr) * st.dv + lane * 4);
-          v.x += f * y.x;
-          v.y += f * y.y;
-          v.z += f * y.z;
-          v.w += f * y.w;
+              p.part + (static_cast<int64_t>(sk) * 256 + rr) * st.dv + lane * 4);
+          v.x += fk * y.x;
+          v.y += fk * y.y;
+          v.z += fk * y.z;
+          v.w += fk * y.w;
         }
       }
     }
@@ -1049,7 +1062,7 @@ int tc_launch(const AttendArgs& all, cudaStream_t stream) {
     q.a.st.cu += s0;
     attend_tc_kernel<T, DP><<<p.ctas, kThreads, kSmem, stream>>>(qm, km, vm, q);
     FASTNN_CUDA_TRY(cudaGetLastError());
-    FASTNN_CUDA_TRY(launch_after(merge_kernel<T>, dim3(p.ctas - 1, 16), dim3(256), stream, q));
+    FASTNN_CUDA_TRY(launch_after(merge_kernel<T>, dim3(p.ctas - 1, 32), dim3(256), stream, q));
   }
   return FASTNN_OK;
 }
