@@ -311,7 +311,7 @@ int fastnn_noalloc_device_status(fastnn_stream_t stream);
  * they are read on the device only, so a captured graph follows their
  * contents. dtype is FASTNN_BF16 or FASTNN_F16 for keys, values, means,
  * queries and outputs alike. k_pages, v_pages and k_mean are contiguous and
- * 16-byte aligned.
+ * 16-byte aligned. The current device is the one that holds them all.
  *
  * What the index arrays may hold (checked on the device, never read out of
  * range): a page id outside [0, n_pages) is a hole, whose positions do not
@@ -403,7 +403,8 @@ int fastnn_store_append(const fastnn_store *store, const void *k, int64_t k_stri
  *   first). Token i of the n_s new tokens of sequence s sees positions below
  *   lens[s] (causal == 0) or below lens[s] - n_s + i + 1 (causal != 0).
  *   q [n][heads_q][d], token stride q_stride, rows 16-byte aligned; heads_q a
- *   multiple of store->heads. out [n][heads_q][dv] contiguous; lse (or NULL)
+ *   multiple of store->heads; max_new * heads_q / heads < 2^31 - 16. out
+ *   [n][heads_q][dv] contiguous; lse (or NULL)
  *   [n][heads_q] float32, the natural logarithm of the sum of the
  *   exponentials. A token that sees nothing gets out = 0, lse = -infinity.
  *   Products and sums in fp32; the weights of the second product are rounded

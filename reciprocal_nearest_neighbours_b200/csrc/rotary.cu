@@ -321,7 +321,7 @@ template <typename T, int V>
 int append_v(const StoreArgs& a, const uint16_t* k, int64_t k_stride, const uint16_t* v,
              int64_t v_stride, int64_t n, int max_new, const RotaryArgs& r, int* status,
              cudaStream_t st) {
-  const int touched = (max_new + a.page - 2) / a.page + 1;
+  const unsigned touched = static_cast<unsigned>((static_cast<int64_t>(max_new) + a.page - 2) / a.page + 1);
   const size_t smem = r.rot ? kAppendRows * r.axes * r.nf * sizeof(float2) : 0;
   append_kernel<T, V><<<dim3(touched, a.heads, a.n_seqs + (status != nullptr)), kAppendThreads, smem, st>>>(
       a, k, k_stride, v, v_stride, n, max_new, r, status);

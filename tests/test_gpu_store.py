@@ -535,6 +535,54 @@ def test_queries_as_part_of_a_fused_projection(news):
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])  # the same bits
 
 
+def test_no_new_tokens():
+    """Calls without a token do nothing, and batches whose sequences all lack one."""
+    st = ref.Store([40, 3], [20, 5], 16, 2, 64, 64, BF16, seed=35, group=2)
+    q, k, v, kp, vp, km, table, before, lens = st.cuda("q", "k", "v", "k_pages", "v_pages", "k_mean", "table",
+                                                       "before", "lens")
+    zero = torch.zeros(3, dtype=torch.int32, device="cuda")
+    fnn.fastnn_store_append(k[:0], v[:0], kp, vp, table, before, zero, 0, k_mean=km)
+    out, lse = fnn.fastnn_attend(q[:0], kp, vp, table, lens, zero, 0)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    assert fnn.fastnn_select_pages(q[:0], km, table, lens, zero, 0, 16, 3).shape == (0, 2, 3)
+    for new in (1, 20):  # rows of no sequence stay as they are, in every kernel
+        fnn.fastnn_store_append(k, v, kp, vp, table, before, zero, new, k_mean=km)
+        out = torch.full((25, 4, 64), 9.0, dtype=BF16, device="cuda")
+        fnn.fastnn_attend(q, kp, vp, table, lens, zero, new, out=out)
+        pages = torch.full((25, 2, 3), -9, dtype=torch.int32, device="cuda")
+        fnn.fastnn_select_pages(q, km, table, lens, zero, new, 16, 3, out=pages)
+        listed = torch.zeros(25, 2, 3, dtype=torch.int32, device="cuda")
+        fnn.fastnn_attend(q, kp, vp, table, lens, zero, new, out=out, pages=listed)
+        assert bool((out == 9).all()) and bool((pages == -9).all())
+    assert torch.equal(kp.cpu(), st.k_pages) and torch.equal(vp.cpu(), st.v_pages) and torch.equal(km.cpu(), st.k_mean)
+
+
+def test_index_arrays_that_make_no_sense_are_survived():
+    """Decreasing and negative offsets, offsets past the batch, lengths past the table: nothing is
+    read or written out of range, and the well-formed sequence is answered."""
+    for new in (2, 40):
+        st = ref.Store([30, 20, 10], [new] * 3, 16, 1, 64, 64, BF16, seed=36, group=2)
+        q, k, v, kp, vp, km, table = st.cuda("q", "k", "v", "k_pages", "v_pages", "k_mean", "table")
+        for cu in ([0, new, -5, 3 * new], [0, new, new, 10 ** 9], [0, new, 2 ** 31 - 1, -2 ** 31],
+                   [0, new, 3 * new + 7, 3 * new + 9]):
+            bad = torch.tensor(cu, dtype=torch.int32, device="cuda")
+            lens = torch.tensor([30 + new, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device="cuda")
+            out, lse = fnn.fastnn_attend(q, kp, vp, table, lens, bad, new)
+            pages = fnn.fastnn_select_pages(q, km, table, lens, bad, new, 16, 3)
+            listed = fnn.fastnn_attend(q, kp, vp, table, lens, bad, new, pages=pages)
+            torch.cuda.synchronize()
+            good = ref.Store([30], [new], 16, 1, 64, 64, BF16, group=2)
+            good.table, good.width, good.n_pages = st.table[:1], st.width, st.n_pages
+            good.k_pages, good.v_pages, good.q = st.k_pages, st.v_pages, st.q[:new]
+            ref.check_attend(out[:new], lse[:new], good)
+            want = ref.select_pages(good, st.k_mean, 3, 0, 1)
+            assert torch.equal(pages[:new].cpu(), want)
+            ref.check_attend(listed[0][:new], listed[1][:new], good, pages=want)
+            ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+            fnn.fastnn_store_append(k, v, kp.clone(), vp.clone(), table, lens, bad, new, k_mean=km.clone(), workspace=ws)
+            assert fnn.fastnn_device_status(ws) == -1
+
+
 def test_many_sequences_at_once():
     """More sequences than one launch of the tensor-core kernel plans for, most without a token."""
     seqs = 700
