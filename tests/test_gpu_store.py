@@ -249,6 +249,22 @@ def test_attend(lens, news, page, heads, group, d, dv, dtype, causal):
     ref.check_attend(out, lse, st, causal)
 
 
+@pytest.mark.parametrize("lens,news,group,d,dtype", [
+    ([5000, 200], [70, 66], 1, 64, BF16),      # lone query tiles, many key tiles, divided between blocks
+    ([9000], [128], 1, 128, F16),
+    ([300, 130, 0, 60], [100, 64, 128, 80], 1, 128, BF16),
+    ([2000, 126], [200, 129], 1, 64, F16),     # a pair, and a lone tile of a few rows
+    ([700, 3000], [40, 33], 2, 32, BF16),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_few_query_tiles_many_keys(lens, news, group, d, dtype, causal):
+    st = ref.Store(lens, news, 64, 2, d, d, dtype, seed=d + group, group=group, tail=1)
+    out, lse = _attend(st, causal)
+    ref.check_attend(out, lse, st, causal)
+    again = _attend(st, causal)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
 @pytest.mark.parametrize("news", [[1, 1], [60, 200]])
 def test_attend_rows_that_see_nothing(news):
     """Sequences of no length, and a batch that claims more new tokens than the store holds."""
