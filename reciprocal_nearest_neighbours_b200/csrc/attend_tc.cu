@@ -361,17 +361,22 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t block)
 
 // Bounded wait for a phase; false, with the abort flag and the status set, if
 // `limit` ns pass or another role has given up. A suspended test may take
-// longer than a short limit, so such limits are watched by polling. (Inlined: a
-// call would have to be possible within either register share.)
+// longer than a short limit; POLL: such limits (below kPolledLimit) are watched by
+// polling, in a kernel of their own.
+// (Inlined: a call would have to be possible within either register share.)
 constexpr uint64_t kPolledLimit = 10000000;
+template <bool POLL>
+__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
+  return POLL ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity);
+}
+template <bool POLL>
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, TcCtl* ctl, int* status,
                                          uint64_t limit) {
-  const bool polled = limit < kPolledLimit;
-  if (polled ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+  if (phase_done<POLL>(bar, parity)) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   for (uint32_t n = 1;; ++n) {
-    if (polled ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
-    if (polled || (n & 63) == 0 || n == 8) {
+    if (phase_done<POLL>(bar, parity)) return true;
+    if (POLL || (n & 63) == 0 || n == 8) {
       if (*reinterpret_cast<volatile int*>(&ctl->abort)) return false;
       if (ptx::globaltimer_ns() - t0 > limit) {
         *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
@@ -384,7 +389,7 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, TcCtl* c
 
 // ---- the kernel -----------------------------------------------------------------
 
-template <typename T, int DP>
+template <typename T, int DP, bool POLL>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TcArgs p) {
@@ -458,7 +463,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   // share (or when a wait ran out).
   auto segment = [&](int k, Seg& e) {
     const int i = k & (kSegRing - 1);
-    if (!__all_sync(0xffffffffu, wait_for(bar(ctl->seg_full[i]), (k / kSegRing) & 1, ctl, a.status, limit)))
+    if (!__all_sync(0xffffffffu, wait_for<POLL>(bar(ctl->seg_full[i]), (k / kSegRing) & 1, ctl, a.status, limit)))
       return false;
     e = ctl->seg[i];
     __syncwarp();
@@ -491,7 +496,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < nt; ++t, ++tiles) {
         const int k0 = (e.jb - 1 - t) * kBlk;
-        ok = __all_sync(0xffffffffu, wait_for(bar(ctl->s_full[w]), sp, ctl, a.status, limit));
+        ok = __all_sync(0xffffffffu, wait_for<POLL>(bar(ctl->s_full[w]), sp, ctl, a.status, limit));
         sp ^= 1;
         if (!ok) break;
         ptx::tc_fence_after();
@@ -568,7 +573,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             m = up;
             if (t > 0) {
               if (C::kOwnP)
-                ok = __all_sync(0xffffffffu, wait_for(bar(ctl->pv_done[w]), pd, ctl, a.status, limit));
+                ok = __all_sync(0xffffffffu, wait_for<POLL>(bar(ctl->pv_done[w]), pd, ctl, a.status, limit));
               ptx::tc_fence_after();
               for (int c = 0; c < nvb * 2; ++c) {
                 uint32_t o[32];
@@ -588,7 +593,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar(ctl->s_free[w]));
           if (t > 0) {  // the weights before these have been used
-            ok = ok && __all_sync(0xffffffffu, wait_for(bar(ctl->pv_done[w]), pd, ctl, a.status, limit));
+            ok = ok && __all_sync(0xffffffffu, wait_for<POLL>(bar(ctl->pv_done[w]), pd, ctl, a.status, limit));
             ptx::tc_fence_after();
           }
           if (!ok) break;
@@ -603,7 +608,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       }
       if (!ok) break;
       if (!C::kOwnP) pd ^= 1;
-      ok = __all_sync(0xffffffffu, wait_for(bar(ctl->pv_done[w]), pd, ctl, a.status, limit));
+      ok = __all_sync(0xffffffffu, wait_for<POLL>(bar(ctl->pv_done[w]), pd, ctl, a.status, limit));
       if (!ok) break;
       ptx::tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
@@ -656,7 +661,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         const bool two = p.tt < e.n;
         const int vmax = e.vmax;
         if (segs > 0) {
-          ok = __all_sync(0xffffffffu, wait_for(bar(ctl->q_empty), q_phase, ctl, a.status, limit));
+          ok = __all_sync(0xffffffffu, wait_for<POLL>(bar(ctl->q_empty), q_phase, ctl, a.status, limit));
           q_phase ^= 1;
           if (!ok) break;
         }
@@ -689,7 +694,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           if (lane == 0) ctl->holes[tiles & (kHoleRing - 1)] = ~there & every;
           for (int kv = 0; kv < 2; ++kv) {
             ok = __all_sync(0xffffffffu,
-                            wait_for(bar(ctl->empty[stage]), phase ^ 1u, ctl, a.status, limit));
+                            wait_for<POLL>(bar(ctl->empty[stage]), phase ^ 1u, ctl, a.status, limit));
             if (!ok) break;
             const uint32_t dst = sbase + C::kRing + stage * C::kTile;
             const int blocks = kv ? nvb : nkb;
@@ -704,7 +709,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             if (!mend) {
               open_stages |= 1u << stage;
             } else {
-              ok = __all_sync(0xffffffffu, wait_for(mb, fix_phase, ctl, a.status, limit));
+              ok = __all_sync(0xffffffffu, wait_for<POLL>(mb, fix_phase, ctl, a.status, limit));
               if (!ok) {  // the copies in flight are waited for before the kernel ends
                 open_stages |= 1u << 31;
                 break;
@@ -745,7 +750,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       uint32_t phase = 0;
       uint32_t pp = 0;  // bit w: the parity that p_full[w] (and s_free[w]) completes next
       auto await = [&](uint64_t& b, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, a.status, limit));
+        return __all_sync(0xffffffffu, wait_for<POLL>(bar(b), parity, ctl, a.status, limit));
       };
       auto product_s = [&](int w, int kstage) {
         const uint64_t qd = ptx::smem_desc_kmajor(sbase + w * C::kTile, 128);
@@ -872,7 +877,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             if (e.jb <= e.ja) continue;  // the item's fixed cost alone
           }
           const int i = k & (kSegRing - 1);
-          if (!wait_for(bar(ctl->seg_empty[i]), ((k / kSegRing) & 1) ^ 1, ctl, a.status, limit)) break;
+          if (!wait_for<POLL>(bar(ctl->seg_empty[i]), ((k / kSegRing) & 1) ^ 1, ctl, a.status, limit)) break;
           ctl->seg[i] = e;
           ptx::mbar_arrive(bar(ctl->seg_full[i]));
           ++k;
@@ -1053,14 +1058,20 @@ int tc_launch(const AttendArgs& all, cudaStream_t stream) {
                  static_cast<uint64_t>(st.page) * st.dv, st.page, 1);
   if (e != FASTNN_OK) return e;
   FASTNN_CUDA_TRY(cudaMemsetAsync(all.status, 0, sizeof(int), stream));
-  FASTNN_CUDA_TRY((allow_smem<attend_tc_kernel<T, DP>>(kSmem)));
+  const bool poll = wait_limit(all.wait_ns) < kPolledLimit;
+  FASTNN_CUDA_TRY(poll ? (allow_smem<attend_tc_kernel<T, DP, true>>(kSmem))
+                       : (allow_smem<attend_tc_kernel<T, DP, false>>(kSmem)));
   for (int s0 = 0; s0 < st.n_seqs; s0 += kMaxSeqs) {
     TcArgs q = p;
     q.a.st.n_seqs = st.n_seqs - s0 < kMaxSeqs ? st.n_seqs - s0 : kMaxSeqs;
     q.a.st.table += static_cast<int64_t>(s0) * st.width;
     q.a.st.lens += s0;
     q.a.st.cu += s0;
-    attend_tc_kernel<T, DP><<<p.ctas, kThreads, kSmem, stream>>>(qm, km, vm, q);
+    if (poll) {
+      attend_tc_kernel<T, DP, true><<<p.ctas, kThreads, kSmem, stream>>>(qm, km, vm, q);
+    } else {
+      attend_tc_kernel<T, DP, false><<<p.ctas, kThreads, kSmem, stream>>>(qm, km, vm, q);
+    }
     FASTNN_CUDA_TRY(cudaGetLastError());
     FASTNN_CUDA_TRY(launch_after(merge_kernel<T>, dim3(p.ctas - 1, 32), dim3(256), stream, q));
   }
