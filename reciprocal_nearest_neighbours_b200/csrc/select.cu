@@ -10,8 +10,9 @@
 // a candidate, all ones: taken whatever its score); a row's keys are held in
 // registers, the select-th largest is found bit by bit (from the highest bit
 // in which they differ), and the pages are written in ascending order.
-//   steps (a few tokens a sequence): half a warp scores a page; up to 512 pages
-//       by the block that picks, more by blocks of 64 pages before the choice.
+//   steps (a few tokens a sequence): half a warp scores a page; for one token and
+//       up to 512 pages in the block that picks, else in blocks of 64 pages before
+//       the choice.
 //       Bound by latency, then by reading the means once. (A cluster of 8 blocks
 //       that shares the pages and picks in one kernel took 30 us for 16
 //       sequences of up to 1024 pages; the two kernels take 24.)
@@ -28,8 +29,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 64;      // tokens, pages of a score tile
 constexpr int kDepth = 32;     // elements of d in shared memory at a time
-constexpr int kStepTokens = 8; // fewer new tokens a sequence: the step kernel (a block each)
-constexpr int kWholeWidth = 512;  // pages that a step's block scores and picks from by itself
+constexpr int kStepTokens = 8; // fewer new tokens a sequence: the step kernel
+constexpr int kWholeWidth = 512;  // pages that a single token's block scores and picks from by itself
 constexpr int kShare = 64;        // pages that it scores where the table is wider
 constexpr int64_t kSlabBytes = 64 << 20;
 
@@ -214,13 +215,13 @@ pick_kernel(SelectArgs a) {
 }
 
 // Steps: half a warp a page, lane l % 16 elements 8 (l % 16) and on, for each of the
-// (fewer than kStepTokens) tokens. WHOLE: a block scores all pages of its sequence
-// and key head and picks from them; else it scores kShare pages, and pick_kernel
-// follows.
+// (fewer than kStepTokens) tokens. WHOLE (one token): a block scores all pages of
+// its sequence and key head and picks from them; else it scores kShare pages, and
+// pick_kernel follows.
 template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kThreads)
 step_kernel(SelectArgs a) {
-  __shared__ uint64_t held_keys[WHOLE ? kStepTokens * kWholeWidth : 1];
+  __shared__ uint64_t held_keys[WHOLE ? kWholeWidth : 1];
   __shared__ __align__(16) double qs[kStepTokens][128];
   const StoreArgs& st = a.st;
   const int s = blockIdx.z, g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -289,7 +290,7 @@ step_kernel(SelectArgs a) {
         if ((lane & 15) == k && p < first + share && p < seen) {
           const uint64_t key = candidate(a, p, seen, there[k], acc[k]);
           if (WHOLE) {
-            held_keys[i * kWholeWidth + p] = key;
+            held_keys[p] = key;
           } else {
             key_row(a, s, i, g)[p] = key;
           }
@@ -300,14 +301,11 @@ step_kernel(SelectArgs a) {
   if constexpr (WHOLE) {
     __syncthreads();
     constexpr int K = kWholeWidth / kThreads;
-    for (int i = 0; i < w.n; ++i) {
-      const int seen = seen_pages(a, w, i);
-      uint64_t held[K];
+    const int seen = seen_pages(a, w, 0);
+    uint64_t held[K];
 #pragma unroll
-      for (int k = 0; k < K; ++k) held[k] = tid * K + k < seen ? held_keys[i * kWholeWidth + tid * K + k] : 0;
-      pick_row<8, K>(a, nullptr, held, seen, static_cast<int64_t>(w.t0) + i, g);
-      __syncthreads();
-    }
+    for (int k = 0; k < K; ++k) held[k] = tid * K + k < seen ? held_keys[tid * K + k] : 0;
+    pick_row<8, K>(a, nullptr, held, seen, w.t0, g);
   }
 }
 
@@ -437,8 +435,10 @@ cudaError_t pick(const SelectArgs& a, cudaStream_t st) {
 }
 
 bool is_step(int max_new) { return max_new < kStepTokens; }
-// Steps over few pages need no scratch.
-bool is_whole(const StoreArgs& st, int max_new) { return is_step(max_new) && st.width <= kWholeWidth; }
+// A single token over few pages needs no scratch and one launch. (16 sequences of
+// 400 pages, 4 key heads: 1 token 19.5 us by one block, 19.8 by two kernels; 7 tokens
+// 80 and 38. Chunk kernels instead of the step's: 50 and 54.)
+bool is_whole(const StoreArgs& st, int max_new) { return max_new == 1 && st.width <= kWholeWidth; }
 
 template <typename T>
 int select_t(const SelectArgs& all, cudaStream_t st) {

@@ -115,7 +115,7 @@ def test_select_refusals(lib):
     assert call(sel=0) == -1 and call(sel=257) == -1 and call(last=0) == -1 and call(first=-1) == -1
     assert call(first=4) == -1 and call(first=2, last=3) == -1 and call(hq=5) == -1
     assert call(out=None) == -1 and call(q=None) == -1 and call(nb=0) == -3
-    assert call(_desc(table_width=4097), ws=None) == -1
+    assert call(_desc(table_width=513), m=1, ws=None) == -1 and call(m=2, ws=None) == -1
     assert call(_desc(k_mean=None)) == -1
     need = lib.fastnn_select_workspace_size(_desc(table_width=1 << 20), 5, 4, 3)  # a key of 8 bytes a page
     assert need >= 2 * 3 * 2 * (1 << 20) * 8 and call(_desc(table_width=1 << 20), nb=need - 1) == -3
