@@ -154,7 +154,7 @@ def _new(like, shape, dtype, stream):
     """A tensor on the device of ``like`` that a launch on ``stream`` (None: the current one)
     writes: on another stream than the one it was allocated on, its memory must not go round
     before that launch is done."""
-    t = like.new_empty(shape, dtype=dtype)
+    t = like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     if stream is not None:
         t.record_stream(stream)
     return t
@@ -318,7 +318,10 @@ def fastnn_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
         _same(dev, torch.float32, "lse", lse)
         if lse.shape != (n, hq) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous [{n}, {hq}]")
-    need = (_bound or _lib()).fastnn_attend_workspace_size(store, n, hq, max_new, select)
+    lib = _bound or _lib()
+    # listed pages need no scratch
+    need = lib.fastnn_attend_workspace_size(store, n, hq, max_new, select) \
+        if pages is None or workspace is not None else _STATUS
     ws = _scratch(need, q, dev, workspace, "fastnn_attend_workspace_size", stream)
     _launch("fastnn_attend", dev, stream, store, q.data_ptr(), qs, n, hq, max_new, causal,
             d ** -0.5 if scale is None else scale, listed, select, out.data_ptr(), lse.data_ptr(),
