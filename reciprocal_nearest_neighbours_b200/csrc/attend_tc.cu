@@ -7,16 +7,18 @@
 // and weights up to kMostSum are as exact in 16-bit floats as weights up to 1.
 // So a tile's weights are formed with the m in force, and only if their sum is
 // above kMostSum is the tile's maximum sought, m raised and O (in tensor
-// memory) rescaled. Then the sum of that tile is at most its 128 keys, so m
-// rises by more than 1 each time and soon no more. And the tiles run from the last key to the first: the tiles with
-// masked places come first, the others run unmasked.
+// memory) rescaled. The sum of that tile is then at most its 128 keys, so m
+// rises by more than 1 each time and soon no more. And the tiles run from the
+// last key to the first: those with masked places come first, the others run
+// unmasked.
 //
 // One CTA per SM, warp-specialised. An item is 2 x 128 query rows (rows are
 // (token, query head of the group), whole tokens only) of one sequence and key
 // head with all their key tiles of 128:
 //   warps 0-3, 4-7: softmax of query tile 0, 1. A thread owns a row: it reads
 //       its 128 scores from tensor memory, and writes the 16-bit weights over
-//       them, as the A operand of the second product; no shuffles.
+//       them (heads of up to 64: beside them), as the A operand of the second
+//       product; no shuffles.
 //   warp 8: loads. Query tiles by one TMA box (64 elements x group x tokens);
 //       K and V tiles page by page (a lane each) into a ring of 128-row tiles.
 //       Pages that do not exist and V rows behind the last visible position
@@ -29,8 +31,12 @@
 // The work is the sequence of all items' key tiles, cut into equal shares, one
 // per CTA (an item costs kItemCost tiles extra). An item that a cut divides
 // leaves normalised partial outputs, which merge_kernel joins.
-// Bound by: the exponentials, 16 a clock and SM against 32 clocks of products
-// per 128 x 16 x 128 step.
+// Bound by: exponentials (16 a clock and SM: 1024 clocks a tile of 128 x 128) and,
+// at 128 elements a head, products (1024 clocks a tile too), whose phases overlap
+// between the two query tiles in part. Measured: 2048 tokens over 16384, 32 / 8
+// heads of 128, 425 us (1.2 PFLOP/s, tensor pipe 61% busy; 500 us under the
+// power cap of a long run); 12288 rows over 196608 keys of 24, values of 8, 700 to 765 us
+// (exponentials 69% busy); 8 x 576 tokens over up to 9792, 12 heads of 64, 180 us.
 // Every wait is bounded; on expiry the kernel records FASTNN_ERR_TIMEOUT,
 // drains what it issued, frees its tensor memory and returns.
 #include <cuda.h>

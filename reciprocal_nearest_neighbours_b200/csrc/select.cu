@@ -20,6 +20,8 @@
 //       thread, both operands as fp64 in shared memory (bound by the fp64 units
 //       and the shared memory that feeds them), then the choice. The keys of a
 //       slab of tokens stay below kSlabBytes, about half of L2.
+// Measured: one token of 16 sequences of 1024 pages, 4 key heads, 25 us; 2048 tokens
+// over 256 pages 70 (scores 50).
 #include "store.cuh"
 
 namespace fastnn {
