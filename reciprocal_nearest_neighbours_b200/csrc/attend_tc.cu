@@ -36,7 +36,7 @@
 // between the two query tiles in part. Measured: 2048 tokens over 16384, 32 / 8
 // heads of 128, 425 us (1.2 PFLOP/s, tensor pipe 61% busy; 500 us under the
 // power cap of a long run); 12288 rows over 196608 keys of 24, values of 8, 700 to 765 us
-// (exponentials 69% busy); 8 x 576 tokens over up to 9792, 12 heads of 64, 180 us.
+// (exponentials 69% busy); 8 x 576 tokens over up to 9792, 12 heads of 64, 172 us.
 // Every wait is bounded; on expiry the kernel records FASTNN_ERR_TIMEOUT,
 // drains what it issued, frees its tensor memory and returns.
 #include <cuda.h>
@@ -60,8 +60,10 @@ constexpr int kThreads = 384;      // three warpgroups: two of softmax, one of l
 constexpr int kSoftRegs = 216;
 constexpr int kOtherRegs = 72;
 constexpr int kBlk = 128;          // rows of a tile (queries, keys)
-constexpr int kItemCost = 2;       // an item's fixed cost, in key tiles
-constexpr int kLeastShare = 4;     // a CTA's share is at least this many tiles
+// An item's fixed cost (its queries, the first scores, the output), in key tiles.
+// 8 images of 576 tokens, with 1 / 2 / 4 / 6 / 8: 184 / 179 / 172 / 173 / 176 us.
+constexpr int kItemCost = 4;
+constexpr int kLeastShare = 2;     // a CTA's share is at least this many tiles and that cost
 constexpr float kMostSum = 256.f;
 constexpr int kMaxCtas = 160;
 constexpr int kHoleRing = 16;      // tiles whose missing pages are remembered
