@@ -12,6 +12,10 @@ others:
     fastnn_store_append(k, v, k_pages, v_pages, page_table, lens, cu, max_new, ...)
     lens += cu[1:] - cu[:-1]
     out, lse = fastnn_attend(q, k_pages, v_pages, page_table, lens, cu, max_new)
+
+A call with ``stream`` launches there: outputs and scratch that it makes are of that
+stream's memory (outputs are also held for the stream that is current). The inputs are the
+caller's to order and to keep until that stream is done with them.
 """
 
 from __future__ import annotations
@@ -151,27 +155,40 @@ def _pages(k_pages, v_pages, dev, dtype):
 
 
 def _new(like, shape, dtype, stream):
-    """A tensor on the device of ``like`` that a launch on ``stream`` (None: the current one)
-    writes: on another stream than the one it was allocated on, its memory must not go round
-    before that launch is done."""
-    t = like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
+    """A tensor on the device of ``like`` that a launch on ``stream`` (None: the current one) is
+    the first to use. It is made of that stream's memory: the current stream's may just have
+    been given back by a call whose kernel is still running there. Hold it until the launch."""
+    if stream is None:
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _result(like, shape, dtype, stream):
+    """As ``_new``, for what the caller gets and will use on the current stream."""
+    t = _new(like, shape, dtype, stream)
     if stream is not None:
-        t.record_stream(stream)
+        t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
-def _scratch(need: int, like, dev, workspace, what: str, stream) -> int:
-    """Address of the call's workspace, 0 for none: _STATUS bytes hold no more than the status
-    word, which nobody reads where the caller brings no workspace."""
+def _scratch(need: int, like, dev, workspace, what: str, stream):
+    """The call's workspace, None for none: _STATUS bytes hold no more than the status word,
+    which nobody reads where the caller brings no workspace. The caller of this holds what it
+    returns until after the launch."""
     if need == 0:
         raise FastNNError(-1, what)
     if workspace is None:
-        return 0 if need == _STATUS else _new(like, need, torch.uint8, stream).data_ptr()
+        return None if need == _STATUS else _new(like, need, torch.uint8, stream)
     if workspace.get_device() != dev:
         raise ValueError(f"the workspace is on {workspace.device}, the tokens on cuda:{dev}")
     if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
         raise FastNNError(-3, "workspace")
-    return workspace.data_ptr()
+    return workspace
+
+
+def _address(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _rotation(pos, freq, layout, scale, n, dev) -> bytes:
@@ -224,7 +241,7 @@ def fastnn_rotary(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, layout
     xs = _rows(x, "x", n, heads, d)
     rot = _rotation(pos, freq, layout, scale, n, dev)
     if out is None:
-        out = _new(x, (n, heads, d), x.dtype, stream)
+        out = _result(x, (n, heads, d), x.dtype, stream)
         to, os = out.data_ptr(), heads * d
     else:
         to, os = _same(dev, x.dtype, "out", out), _rows(out, "out", n, heads, d)
@@ -266,7 +283,7 @@ def fastnn_store_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
         ws = _scratch(FASTNN_STORE_APPEND_WORKSPACE, k, dev, workspace, "", stream)
     _bound or _lib()
     _launch("fastnn_store_append", dev, stream, store, k.data_ptr(), ks, at_v, vs, n, max_new, rot,
-            ws, FASTNN_STORE_APPEND_WORKSPACE)
+            _address(ws), FASTNN_STORE_APPEND_WORKSPACE)
 
 
 def fastnn_attend_workspace_size(n: int, heads_q: int, heads: int, d: int, dv: int, n_seqs: int,
@@ -307,13 +324,13 @@ def fastnn_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
             raise ValueError(f"pages must be [{n}, {heads}, select], got {tuple(pages.shape)}")
         select = pages.shape[2]
     if out is None:
-        out = _new(q, (n, hq, dv), dtype, stream)
+        out = _result(q, (n, hq, dv), dtype, stream)
     else:
         _same(dev, dtype, "out", out)
         if out.shape != (n, hq, dv) or not out.is_contiguous():
             raise ValueError(f"out must be contiguous [{n}, {hq}, {dv}]")
     if lse is None:
-        lse = _new(q, (n, hq), torch.float32, stream)
+        lse = _result(q, (n, hq), torch.float32, stream)
     else:
         _same(dev, torch.float32, "lse", lse)
         if lse.shape != (n, hq) or not lse.is_contiguous():
@@ -325,7 +342,7 @@ def fastnn_attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     ws = _scratch(need, q, dev, workspace, "fastnn_attend_workspace_size", stream)
     _launch("fastnn_attend", dev, stream, store, q.data_ptr(), qs, n, hq, max_new, causal,
             d ** -0.5 if scale is None else scale, listed, select, out.data_ptr(), lse.data_ptr(),
-            ws, need)
+            _address(ws), need)
     return out, lse
 
 
@@ -352,7 +369,7 @@ def fastnn_select_pages(q: torch.Tensor, k_mean: torch.Tensor, page_table: torch
     qs = _rows(q, "q", n, hq, d)
     store = _describe(code, dev, page_table, lens, cu, n_pages, heads, page, d, 8, None, None, mean)
     if out is None:
-        out = _new(q, (n, heads, select), _I32, stream)
+        out = _result(q, (n, heads, select), _I32, stream)
     else:
         _index(out, "out", 3, dev)
         if out.shape != (n, heads, select):
@@ -360,5 +377,5 @@ def fastnn_select_pages(q: torch.Tensor, k_mean: torch.Tensor, page_table: torch
     need = (_bound or _lib()).fastnn_select_workspace_size(store, n, hq, max_new)
     ws = _scratch(need, q, dev, workspace, "fastnn_select_workspace_size", stream)
     _launch("fastnn_select_pages", dev, stream, store, q.data_ptr(), qs, n, hq, max_new, causal,
-            keep_first, keep_last, select, out.data_ptr(), ws, need)
+            keep_first, keep_last, select, out.data_ptr(), _address(ws), need)
     return out

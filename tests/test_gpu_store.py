@@ -4,6 +4,7 @@ plain 64-bit forms of tests/_store.py at the sizes and masks where they can go w
 from __future__ import annotations
 
 import math
+import threading
 
 import pytest
 import torch
@@ -706,3 +707,72 @@ def test_refusals_of_shapes_types_and_devices():
         fnn.fastnn_select_pages(q, z(4, 2, 64), table, lens, cu, 3, 16, 2, keep_first=2)
     with pytest.raises(ValueError):
         fnn.fastnn_select_pages(q, z(4, 3, 64), table, lens, cu, 3, 16, 2)
+
+
+# ---- calls at the same time --------------------------------------------------------------------
+
+def _twins(lens, news, seed):
+    """Two stores of the same sizes with other contents, on the GPU, and what each call on them
+    answers by itself (attention, chosen pages, attention over them)."""
+    both = []
+    for i in range(2):
+        st = ref.Store(lens, news, 16, 2, 64, 64, BF16, seed=seed + i, group=2)
+        args = st.cuda("q", "k_pages", "v_pages", "table", "lens", "cu")
+        km = st.k_mean.cuda()
+
+        def calls(stream=None, args=args, km=km, st=st):
+            q, kp, vp, table, ln, cu = args
+            pages = fnn.fastnn_select_pages(q, km, table, ln, cu, st.max_new, 16, 6, stream=stream)
+            return (*fnn.fastnn_attend(*args, st.max_new, stream=stream), pages,
+                    *fnn.fastnn_attend(*args, st.max_new, pages=pages, stream=stream))
+        want = calls()
+        ref.check_attend(want[0], want[1], st)
+        assert torch.equal(want[2].cpu(), ref.select_pages(st, st.k_mean, 6, 0, 1))
+        both.append((calls, want))
+    torch.cuda.synchronize()
+    return both
+
+
+BATCHES = [([9000, 3000], [1, 1]), ([700, 300], [130, 70])]  # partial outputs of splits, of shares
+
+
+@pytest.mark.parametrize("lens,news", BATCHES)
+def test_a_call_on_another_stream_right_after_one_on_the_current(lens, news):
+    (here, want_here), (there, want_there) = _twins(lens, news, 41)
+    side = torch.cuda.Stream()
+    busy = torch.randn(2048, 2048, device="cuda")
+    size = max(1 << 20, fnn.fastnn_attend_workspace_size(sum(news), 4, 2, 64, 64, 2, max(news),
+                                                         -(-(max(lens) + max(news)) // 16), 16))
+    torch.cuda.synchronize()
+    for turn in range(24):
+        if turn % 2:  # the side stream is late: what it uses must still be there
+            with torch.cuda.stream(side):
+                for _ in range(4):
+                    torch.mm(busy, busy)
+        got_here = here()
+        got_there = there(stream=side)
+        fills = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        fills += [torch.full_like(x, 3) for x in want_here for _ in range(2)]
+        del fills
+        torch.cuda.current_stream().wait_stream(side)
+        for got, want in zip((*got_here, *got_there), (*want_here, *want_there)):
+            assert torch.equal(got, want), turn
+
+
+@pytest.mark.parametrize("lens,news", BATCHES)
+def test_calls_from_two_threads_on_one_stream(lens, news):
+    both = _twins(lens, news, 51)
+    wrong = []
+
+    def many(calls, want):
+        for turn in range(40):
+            for got, w in zip(calls(), want):
+                if not torch.equal(got, w):
+                    wrong.append(turn)
+
+    threads = [threading.Thread(target=many, args=x) for x in both]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import ctypes
+import weakref
 
 import pytest
 import torch
@@ -156,3 +157,76 @@ def test_rotary_frequencies():
     assert f.dtype == torch.float64 and f.tolist() == [0.5, 0.25, 0.125, 0.0625]
     assert fnn.fastnn_rotary_frequencies(8, base=16.0, axes=2, device="cpu").tolist() == [1.0, 0.25]
     assert fnn.fastnn_rotary_frequencies(8, long_base=81.0, device="cpu")[1].item() == pytest.approx(1 / 3)
+
+
+class _Side:
+    """Stands for a stream other than the current one."""
+    device = torch.device("cuda", 0)
+    cuda_stream = 77
+
+
+@pytest.fixture
+def marshalled(lib, monkeypatch):
+    """Runs the binding on CPU tensors up to the launch. Yields the launches: for each the tensors
+    that the call has made, as (alive at the launch, stream whose memory it is, shape, streams that
+    its memory is kept for)."""
+    home, current, made, launches = object(), [], [], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    real = torch.Tensor.new_empty
+
+    def new_empty(self, *args, **kw):
+        t = real(self, *args, **kw)
+        made.append([weakref.ref(t), current[-1] if current else home, tuple(t.shape), []])
+        return t
+
+    def record_stream(self, stream):
+        for m in made:
+            if m[0]() is self:
+                m[3].append(stream)
+
+    def launch(what, dev, stream, *args):
+        launches.append([(ref() is not None, where, shape, tuple(kept)) for ref, where, shape, kept in made])
+        made.clear()
+
+    monkeypatch.setattr(_store, "_device", lambda t: -1)  # a CPU tensor's get_device()
+    monkeypatch.setattr(_store, "_launch", launch)
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: current[-1] if current else home)
+    monkeypatch.setattr(torch.Tensor, "new_empty", new_empty)
+    monkeypatch.setattr(torch.Tensor, "record_stream", record_stream)
+    return home, launches
+
+
+@pytest.mark.parametrize("stream", [None, _Side()], ids=["current", "side"])
+def test_memory_of_a_call_belongs_to_its_stream_and_is_held_until_the_launch(marshalled, stream):
+    """Scratch that goes back to the allocator before the launch, or that comes from the memory of
+    another stream than the launch's, may be in use by another kernel at the same time."""
+    home, launches = marshalled
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    store = z(9, 2, 16, 64), z(9, 2, 16, 64), i(2, 4096), i(2), i(3)
+    for new in (1, 70):  # partial outputs of splits, of the tensor-core kernel
+        q = z(2 * new, 4, 64)
+        out, lse = fnn.fastnn_attend(q, *store, new, stream=stream)
+        pages = fnn.fastnn_select_pages(q, z(9, 2, 64), *store[2:], new, 16, 4, stream=stream)
+        fnn.fastnn_attend(q, *store, new, pages=pages, stream=stream)
+        fnn.fastnn_attend(q, *store, new, out=out, lse=lse, stream=stream)
+        fnn.fastnn_rotary(q, i(2 * new), torch.zeros(4, dtype=torch.float64), stream=stream)
+    counts = [3, 2, 2, 1, 1] * 2  # outputs and scratch
+    assert [len(made) for made in launches] == counts
+    for made in launches:
+        for alive, where, shape, kept in made:
+            assert alive, shape
+            assert where is (home if stream is None else stream), shape
+            if stream is not None and len(shape) > 1:  # an output: read on the current stream next
+                assert kept == (home,), shape
