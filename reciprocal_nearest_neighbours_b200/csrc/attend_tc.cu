@@ -75,7 +75,7 @@ struct Tc {
   static constexpr int kRing = 2 * kTile;          // after the two query tiles
   static constexpr int kCtl = kRing + kStages * kTile;
   static constexpr int kBlock = kBlk * 128;        // bytes of a 64-element column block
-  // Of every 16 pairs of weights, so many by polynomial (12 instructions a pair
+  // Of every 16 pairs of weights, so many by polynomial (14 instructions a pair
   // against 16 clocks of the special-function unit). Measured with 2 / 5 / 7:
   // 12288 queries over 196608 keys of 24 765 / 800 / 822 us; with 0 / 2 / 5: 2048
   // over 16384, 32 heads of 128, 434 / 425 / 432 us.
@@ -285,11 +285,15 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
 // nearest whole number (the sum with 1.5 * 2^23 leaves it in the low mantissa
 // bits), 2^f by its minimax polynomial of degree 5 on [-1/2, 1/2] (found by
 // Remez exchange on the relative error; in fp32 2^-22.2, as good as the unit's),
-// and j added to the exponent. x <= 8 here; below -126 the result is 2^-126,
-// nothing beside a row's largest weight of at least 2^-8.
+// and j added to the exponent, which holds for x in [-126, 127]. Below, the result
+// is 2^-126, nothing beside a row's largest weight of at least 2^-8. Above 8 =
+// log2(kMostSum) any large result serves, since the tile's weights are formed
+// anew by the unit then: 2^kPolyMost stands for all x beyond (a key may score any
+// amount above the maximum in force), and for NaN, which fminf drops.
+constexpr float kPolyMost = 64.f;
 __device__ __forceinline__ float2 ex2_pair(uint64_t x) {
   float2 v = halves(x);
-  x = pair(fmaxf(v.x, -126.f), fmaxf(v.y, -126.f));
+  x = pair(fmaxf(fminf(v.x, kPolyMost), -126.f), fmaxf(fminf(v.y, kPolyMost), -126.f));
   const uint64_t magic = pair(12582912.f, 12582912.f);
   const uint64_t t = add2(x, magic);
   const uint64_t f = sub2(x, sub2(t, magic));

@@ -776,3 +776,44 @@ def test_calls_from_two_threads_on_one_stream(lens, news):
     for t in threads:
         t.join()
     assert not wrong
+
+
+# ---- scores far above those before -------------------------------------------------------------
+
+@pytest.mark.parametrize("gap", [100, 127.5, 128.2, 129, 150, 200, 255, 300, 384, 400, 520, 3000])
+@pytest.mark.parametrize("d,dtype", [(64, BF16), (64, F16), (128, BF16), (128, F16)])
+def test_attend_one_key_far_above_all_others(gap, d, dtype):
+    """All keys zero but one, which scores ``gap`` (base 2) with every query: it has the weight, at
+    every place that the kernels treat in a way of its own, in the key tiles without a mask too."""
+    st = ref.Store([192], [64], 64, 1, d, d, dtype, seed=int(gap), group=1)
+    st.q.zero_()
+    st.q[:, :, 0] = 16.0
+    q, vp, table, lens, cu = st.cuda("q", "v_pages", "table", "lens", "cu")
+    scale = gap * math.log(2.0) / 256
+    for at in [*range(9), 31, 32, 33, 66, 96, 127, 128, 160]:
+        st.k_pages.zero_()
+        st.k_pages[int(st.table[0, at // 64]), 0, at % 64, 0] = 16.0
+        for causal in (False, True):
+            out, lse = fnn.fastnn_attend(q, st.k_pages.cuda(), vp, table, lens, cu, 64, causal=causal, scale=scale)
+            # every token sees the key; the others' weights, 2^-gap each, are below half a step
+            want = st.v_pages[int(st.table[0, at // 64]), 0, at % 64]
+            assert bool((out.cpu() == want).all()), (at, causal)
+            # the product is exact; scale, its product with log2 e, the score, its way back to nats
+            # and the result are rounded to fp32 once each, the exponential of 0 and log2 are good to 2^-21
+            off = (lse.cpu().double() - gap * math.log(2.0)).abs().max()
+            assert float(off) <= 6 * 2.0 ** -24 * gap + 2.0 ** -21, (at, causal)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+def test_attend_a_few_scores_far_above_all_others(d, dtype):
+    """Keys of ordinary size and, for a few rows of a few warps, one far larger: over several tiles."""
+    for seed, (scale, at) in enumerate(((2.0, 0), (6.0, 2), (20.0, 129), (40.0, 33), (3.0, 256))):
+        st = ref.Store([500], [70], 64, 1, d, d, dtype, seed=60 + seed, group=2)
+        st.k_pages *= 0.05
+        ph = int(st.table[0, at // 64])
+        st.k_pages[ph, 0, at % 64] = 0
+        st.k_pages[ph, 0, at % 64, 0] = 8.0
+        st.q[:, :, 0] = 0
+        st.q[::9, :, 0] = 8.0  # one row in nine
+        out, lse = _attend(st, causal=bool(seed & 1), scale=scale)
+        ref.check_attend(out, lse, st, bool(seed & 1), scale=scale)
