@@ -411,7 +411,8 @@ int fastnn_store_append(const fastnn_store *store, const void *k, int64_t k_stri
  *   to dtype (relative 2^-9 for bf16, far below the rounding of a result that
  *   averages them); out is rounded once.
  *   Keys and values at positions that some token of the call sees must be
- *   finite; what lies behind lens in a page is never used.
+ *   finite; what lies behind lens in a page is never used. NaN in a row of q
+ *   makes that row of out and lse NaN (where it sees anything), and no other.
  *   pages (or NULL): [n][heads][select] logical page numbers (position / page),
  *   as fastnn_select_pages writes them: the token then sees only the positions
  *   of the pages listed for its key head. Entries outside its sequence's pages

@@ -550,13 +550,13 @@ combine_kernel(AttendArgs a) {
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < kWarps; ++q) top = fmaxf(top, tops[q]);
-  const bool any = top > -INFINITY;
   float sum = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   const int c = lane * 4;
 #pragma unroll 4
   for (int i = warp; i < parts; i += kWarps) {
-    const float f = any ? ex2(a.part_lse[i * step + row] - top) : 0.f;
+    const float z = a.part_lse[i * step + row];  // NaN makes the row NaN, though fmaxf drops it
+    const float f = z == -INFINITY ? 0.f : ex2(z - top);
     const float4 y = c < st.dv ? *reinterpret_cast<const float4*>(a.part + (i * step + row) * st.dv + c)
                                : make_float4(0.f, 0.f, 0.f, 0.f);
     sum += f;
@@ -578,11 +578,11 @@ combine_kernel(AttendArgs a) {
     v.z += y.z;
     v.w += y.w;
   }
-  const float inv = any ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   if (c < st.dv)
     *reinterpret_cast<uint2*>(a.out + row * st.dv + c) =
         make_uint2(Half16<T>::pack(v.x * inv, v.y * inv), Half16<T>::pack(v.z * inv, v.w * inv));
-  if (lane == 0 && a.lse) a.lse[row] = any ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+  if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
 // Groups of 8 query rows of a block: one if no block would have more rows.

@@ -969,7 +969,7 @@ merge_kernel(const __grid_constant__ TcArgs p) {
       float up = fmaxf(top, z);
 #pragma unroll
       for (int o = 16; o; o >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
-      if (up == -INFINITY) continue;
+      if (!__any_sync(0xffffffffu, z != -INFINITY)) continue;  // NaN is a part, too: fmaxf drops it
       const float old = top == -INFINITY ? 0.f : ex2(top - up);
       sum *= old;
       v.x *= old;
@@ -977,7 +977,7 @@ merge_kernel(const __grid_constant__ TcArgs p) {
       v.z *= old;
       v.w *= old;
       top = up;
-      const float f = slot >= 0 ? ex2(z - up) : 0.f;
+      const float f = z == -INFINITY ? 0.f : ex2(z - up);
       unsigned some = __ballot_sync(0xffffffffu, slot >= 0);
       while (some) {
         const int k = __ffs(some) - 1;
@@ -995,12 +995,12 @@ merge_kernel(const __grid_constant__ TcArgs p) {
         }
       }
     }
-    const float inv = top == -INFINITY ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (lane * 4 < st.dv)
       *reinterpret_cast<uint2*>(a.out + row * st.dv + lane * 4) =
           make_uint2(Half16<T>::pack(v.x * inv, v.y * inv), Half16<T>::pack(v.z * inv, v.w * inv));
     if (lane == 0 && a.lse)
-      a.lse[row] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+      a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
   }
 }
 

@@ -817,3 +817,58 @@ def test_attend_a_few_scores_far_above_all_others(d, dtype):
         st.q[::9, :, 0] = 8.0  # one row in nine
         out, lse = _attend(st, causal=bool(seed & 1), scale=scale)
         ref.check_attend(out, lse, st, bool(seed & 1), scale=scale)
+
+
+# ---- queries that are no numbers ---------------------------------------------------------------
+
+@pytest.mark.parametrize("lens,news,group,d", [
+    ([40], [70], 2, 64),           # chunks: one tile, several, divided between blocks
+    ([700, 300], [130, 66], 1, 128),
+    ([9000, 20], [66, 70], 1, 64),
+    ([9000], [64], 1, 128),
+    ([40, 7], [1, 1], 4, 64),      # single tokens: one split, several
+    ([9000, 3000], [1, 1], 2, 64),
+    ([2999, 40], [1, 3], 4, 128),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_nan_in_a_query_is_the_answer_of_its_row_alone(lens, news, group, d, causal):
+    st = ref.Store(lens, news, 64, 2, d, d, BF16, seed=70, group=group)
+    clean, lse_clean = _attend(st, causal)
+    ref.check_attend(clean, lse_clean, st, causal)
+    whole = st.q.clone()
+    bad = torch.zeros(st.n, 2 * group, dtype=torch.bool)
+    bad[0, 0] = bad[st.n // 2, -1] = bad[st.n - 1, group] = True
+    st.q[bad] = float("nan")
+    out, lse = _attend(st, causal)
+    gone = bad.cuda()
+    assert bool(out[gone].isnan().all()) and bool(lse[gone].isnan().all())
+    out[gone], lse[gone] = clean[gone], lse_clean[gone]
+    st.q = whole
+    ref.check_attend(out, lse, st, causal)
+
+
+def test_nan_in_a_query_that_sees_nothing():
+    for news in ([1, 1], [70, 3]):
+        st = ref.Store([0, 0], news, 16, 1, 64, 64, F16, seed=3)
+        st.q[:] = float("nan")
+        st.lens = torch.tensor([0, -3], dtype=torch.int32)
+        out, lse = _attend(st, causal=False)
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("news,select", [([1, 1], 2), ([1, 3], 24), ([90, 5], 6)])
+def test_nan_in_a_query_over_listed_pages(news, select):
+    """The lowest pages are taken, all scores being NaN; splits in one block and in clusters."""
+    st = ref.Store([2000, 300], news, 64, 2, 64, 64, F16, seed=71, group=4)
+    q, km, table, lens, cu = st.cuda("q", "k_mean", "table", "lens", "cu")
+    q[0] = float("nan")
+    pages = fnn.fastnn_select_pages(q, km, table, lens, cu, st.max_new, 64, select)
+    st.q = q.cpu()
+    want = ref.select_pages(st, st.k_mean, select, 0, 1)
+    assert torch.equal(pages.cpu(), want)
+    out, lse = _attend(st, pages=pages)
+    assert bool(out[0].isnan().all()) and bool(lse[0].isnan().all())
+    st.q[0] = 0  # the others' answers
+    clean, lse_clean = _attend(st, pages=pages)
+    out[0], lse[0] = clean[0], lse_clean[0]
+    ref.check_attend(out, lse, st, pages=want)
