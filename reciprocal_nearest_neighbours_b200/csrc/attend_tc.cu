@@ -550,11 +550,14 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         load();
         // Most tiles need no maximum of their own: while their weights, by the
         // maximum in force, sum to no more than kMostSum, none of them is larger.
+        // Rows that are no token's have no say: what lies there (another
+        // sequence's queries, whatever shared memory held) must not decide how
+        // the others' weights are formed.
         float sum = 0.f;
         bool again = edge || t == 0;
         if (!again) {
           sum = weigh(std::integral_constant<int, C::kPolyPairs>{});
-          again = __any_sync(0xffffffffu, sum > kMostSum || m == -INFINITY);
+          again = __any_sync(0xffffffffu, real && (sum > kMostSum || m == -INFINITY));
         }
         if (again) {
           load();  // the scores are still there: the weights have not been stored
@@ -577,7 +580,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
               top[c] = ptx::fmax3(top[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
           }
           const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-          if (__any_sync(0xffffffffu, mx > m)) {
+          if (__any_sync(0xffffffffu, real && mx > m)) {
             // Raise the maximum, and scale what was summed with the one before.
             const float up = fmaxf(m, mx);
             const float f = m == up ? 1.f : ex2(m - up);

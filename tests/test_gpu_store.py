@@ -872,3 +872,24 @@ def test_nan_in_a_query_over_listed_pages(news, select):
     clean, lse_clean = _attend(st, pages=pages)
     out[0], lse[0] = clean[0], lse_clean[0]
     ref.check_attend(out, lse, st, pages=want)
+
+
+# ---- what earlier kernels leave in shared memory -----------------------------------------------
+
+@pytest.mark.parametrize("group", [3, 5, 7, 48])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_the_same_bits_whatever_ran_before(group, d):
+    """Groups that do not divide a tile of 128 rows leave rows of it unfilled: what an earlier call
+    left there has no part in how the others are computed."""
+    before = ref.Store([64] * 8, [300] * 8, 64, 8, d, d, BF16, seed=80)  # every SM, whole tiles
+    fill = before.cuda("q", "k_pages", "v_pages", "table", "lens", "cu")
+    st = ref.Store([900, 300], [130, 60], 64, 2, d, d, BF16, seed=81, group=group)
+    args = st.cuda("q", "k_pages", "v_pages", "table", "lens", "cu")
+    got = []
+    for x in (0.0, float("nan"), 300.0, -300.0):
+        fill[0].fill_(x)
+        fnn.fastnn_attend(*fill, before.max_new, causal=False)
+        got.append(fnn.fastnn_attend(*args, st.max_new, causal=False))
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+    assert not bool(got[0][1].isnan().any())
