@@ -311,7 +311,8 @@ int fastnn_noalloc_device_status(fastnn_stream_t stream);
  * they are read on the device only, so a captured graph follows their
  * contents. dtype is FASTNN_BF16 or FASTNN_F16 for keys, values, means,
  * queries and outputs alike. k_pages, v_pages and k_mean are contiguous and
- * 16-byte aligned. The current device is the one that holds them all.
+ * 16-byte aligned. The current device is the one that holds them all. A batch
+ * has at most 2^30 tokens, max_new (where n > 0) is 1 .. n.
  *
  * What the index arrays may hold (checked on the device, never read out of
  * range): a page id outside [0, n_pages) is a hole, whose positions do not

@@ -604,8 +604,7 @@ int rows_launch(const AttendArgs& a, cudaStream_t st) {
   static_assert(D::kBlocks * (S::kTotal + 1024) <= 228 * 1024, "the blocks fit an SM");
   FASTNN_CUDA_TRY((allow_smem<attend_rows_kernel<T, DP, NT, SEL, FULL, MANY>>(S::kTotal)));
   const int64_t tiles = row_tiles(a);
-  if (tiles * a.splits > INT32_MAX || static_cast<int64_t>(a.max_new) * a.group > INT32_MAX - 16)
-    return FASTNN_ERR_INVALID;  // rows are counted in 32 bits
+  if (tiles * a.splits > INT32_MAX) return FASTNN_ERR_INVALID;
   const dim3 grid(static_cast<unsigned>(tiles * a.splits), a.st.heads, a.st.n_seqs);
   if (SEL && a.splits > 1) {
     FASTNN_CUDA_TRY(launch_cluster(attend_rows_kernel<T, DP, NT, SEL, FULL, MANY>, grid, dim3(kThreads), S::kTotal,

@@ -67,9 +67,11 @@ int rotation_args(const fastnn_rotation* r, int d, int inverse, RotaryArgs& a) {
   return FASTNN_OK;
 }
 
-// Checks of a ragged batch of new tokens.
+// Checks of a ragged batch of new tokens. The kernels count tokens in 32 bits, up to
+// a tile or a slab (at most 2^23 tokens) past the last one.
+constexpr int64_t kMaxTokens = int64_t{1} << 30;
 int batch_sizes(int64_t n, int max_new) {
-  if (n < 0 || n > INT32_MAX) return FASTNN_ERR_INVALID;
+  if (n < 0 || n > kMaxTokens) return FASTNN_ERR_INVALID;
   if (n > 0 && (max_new < 1 || max_new > n)) return FASTNN_ERR_INVALID;
   return FASTNN_OK;
 }
@@ -105,6 +107,12 @@ int attend_sizes(const fastnn_store* s, int64_t n, int heads_q, int max_new, int
   if (heads_q < 1 || heads_q % s->heads || heads_q > 65535 || select < 0 || select > 65535)
     return FASTNN_ERR_INVALID;
   return FASTNN_OK;
+}
+
+// fastnn_attend alone: the rows (token, head of a group) of a sequence, which are
+// counted in 32 bits, up to a tile past the last one.
+int attend_rows(const fastnn_store* s, int heads_q, int max_new) {
+  return static_cast<int64_t>(max_new) * (heads_q / s->heads) > INT32_MAX - 16 ? FASTNN_ERR_INVALID : FASTNN_OK;
 }
 
 size_t part_bytes(const AttendArgs& a) {
@@ -165,6 +173,7 @@ size_t fastnn_attend_workspace_size(const fastnn_store* store, int64_t n, int he
                                     int select) {
   if (attend_sizes(store, n, heads_q, max_new, select) != FASTNN_OK) return 0;
   if (n == 0) return kAlign;
+  if (attend_rows(store, heads_q, max_new) != FASTNN_OK) return 0;
   static const int32_t some = 0;
   return attend_bytes(attend_args(store, n, heads_q, max_new, select ? &some : nullptr, select));
 }
@@ -176,6 +185,7 @@ int fastnn_attend(const fastnn_store* store, const void* q, int64_t q_stride, in
   FASTNN_TRY(attend_sizes(store, n, heads_q, max_new, select));
   if (!std::isfinite(scale) || (pages != nullptr) != (select > 0)) return FASTNN_ERR_INVALID;
   if (n == 0) return FASTNN_OK;
+  FASTNN_TRY(attend_rows(store, heads_q, max_new));
   FASTNN_TRY(row_checks(q, q_stride, static_cast<int64_t>(heads_q) * store->d));
   if (!store->k_pages || !aligned(store->k_pages, 16) || !store->v_pages ||
       !aligned(store->v_pages, 16) || !store->page_table || !store->lens || !store->cu || !out ||

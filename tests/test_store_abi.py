@@ -230,3 +230,28 @@ def test_memory_of_a_call_belongs_to_its_stream_and_is_held_until_the_launch(mar
             assert where is (home if stream is None else stream), shape
             if stream is not None and len(shape) > 1:  # an output: read on the current stream next
                 assert kept == (home,), shape
+
+
+def test_batches_beyond_what_the_kernels_count_are_refused(lib):
+    """Tokens and rows are counted in 32 bits, tiles of them rounded up: every kernel's path refuses
+    what does not fit, before anything is launched."""
+    big, top = 1 << 60, 1 << 30
+
+    def attend(n, hq, m, scale=1.0, pages=None, sel=0, **kw):
+        s = _desc(**kw)
+        return (lib.fastnn_attend(s, FAKE, 1 << 20, n, hq, m, 1, scale, pages, sel, FAKE, FAKE, FAKE, big, None),
+                lib.fastnn_attend_workspace_size(s, n, hq, m, sel))
+    for scale in (1.0, -1.0):  # the tensor-core kernel's calls, the other's
+        for pages, sel in ((None, 0), (FAKE, 4)):
+            for n, hq, m in ((top + 1, 2, 1), (top + 1, 2, top + 1), ((1 << 31) - 1, 2, (1 << 31) - 1),
+                             (top, 4, top), (1 << 29, 8, 1 << 29), ((1 << 31) // 6, 12, (1 << 31) // 6)):
+                assert attend(n, hq, m, scale, pages, sel) == (-1, 0), (n, hq, m)
+    s = _desc()
+    for n, m in ((top + 1, 1), (top + 1, top + 1), ((1 << 31) - 1, (1 << 31) - 1)):
+        assert lib.fastnn_select_pages(s, FAKE, 1 << 20, n, 2, m, 1, 0, 1, 4, FAKE, FAKE, big, None) == -1
+        assert lib.fastnn_select_workspace_size(s, n, 2, m) == 0
+        assert lib.fastnn_store_append(s, FAKE, 8192, FAKE, 8192, n, m, None, FAKE, 256, None) == -1
+    # the largest that are taken
+    assert lib.fastnn_attend_workspace_size(s, top, 2, top, 0) > 0
+    assert lib.fastnn_attend_workspace_size(s, top, 4, top - 9, 0) > 0
+    assert lib.fastnn_select_workspace_size(s, top, 2, top) > 0
