@@ -81,6 +81,11 @@ int row_checks(const void* x, int64_t stride, int64_t width) {
   return FASTNN_OK;
 }
 
+bool index_arrays(const fastnn_store* s) {
+  return s->page_table && s->lens && s->cu && aligned(s->page_table, 4) && aligned(s->lens, 4) && aligned(s->cu, 4);
+}
+bool rotation_arrays(const RotaryArgs& r) { return r.pos && r.freq && aligned(r.pos, 4) && aligned(r.freq, 8); }
+
 #define FASTNN_TRY(expr)              \
   do {                                \
     int rc_ = (expr);                 \
@@ -139,7 +144,7 @@ int fastnn_rotary(const void* x, int64_t x_stride, int64_t n, int heads, int d, 
   if (r.rot == 0) return FASTNN_ERR_INVALID;
   if (n == 0) return FASTNN_OK;
   const int64_t width = static_cast<int64_t>(heads) * d;
-  if (!r.pos || !r.freq) return FASTNN_ERR_INVALID;
+  if (!rotation_arrays(r)) return FASTNN_ERR_INVALID;
   if (!x || !out || !aligned(x, 2) || !aligned(out, 2) || x_stride < width || out_stride < width)
     return FASTNN_ERR_INVALID;
   if (x == out && x_stride != out_stride) return FASTNN_ERR_INVALID;
@@ -156,12 +161,12 @@ int fastnn_store_append(const fastnn_store* store, const void* k, int64_t k_stri
   RotaryArgs r{};
   if (rotation) FASTNN_TRY(rotation_args(rotation, store->d, 0, r));
   if (n == 0) return FASTNN_OK;
-  if (r.rot > 0 && (!r.pos || !r.freq)) return FASTNN_ERR_INVALID;
+  if (r.rot > 0 && !rotation_arrays(r)) return FASTNN_ERR_INVALID;
   FASTNN_TRY(row_checks(k, k_stride, static_cast<int64_t>(store->heads) * store->d));
   FASTNN_TRY(row_checks(v, v_stride, static_cast<int64_t>(store->heads) * store->dv));
   if (!store->k_pages || !aligned(store->k_pages, 16) || !store->v_pages ||
-      !aligned(store->v_pages, 16) || !aligned(store->k_mean, 16) || !store->page_table ||
-      !store->lens || !store->cu || !aligned(workspace, kAlign))
+      !aligned(store->v_pages, 16) || !aligned(store->k_mean, 16) || !index_arrays(store) ||
+      !aligned(workspace, kAlign))
     return FASTNN_ERR_INVALID;
   if (workspace && workspace_bytes < FASTNN_STORE_APPEND_WORKSPACE) return FASTNN_ERR_CAPACITY;
   return launch_store_append(store_args(store), store->dtype, static_cast<const uint16_t*>(k),
@@ -188,7 +193,7 @@ int fastnn_attend(const fastnn_store* store, const void* q, int64_t q_stride, in
   FASTNN_TRY(attend_rows(store, heads_q, max_new));
   FASTNN_TRY(row_checks(q, q_stride, static_cast<int64_t>(heads_q) * store->d));
   if (!store->k_pages || !aligned(store->k_pages, 16) || !store->v_pages ||
-      !aligned(store->v_pages, 16) || !store->page_table || !store->lens || !store->cu || !out ||
+      !aligned(store->v_pages, 16) || !index_arrays(store) || !aligned(pages, 4) || !out ||
       !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, kAlign))
     return FASTNN_ERR_INVALID;
   AttendArgs a = attend_args(store, n, heads_q, max_new, pages, select);
@@ -227,8 +232,8 @@ int fastnn_select_pages(const fastnn_store* store, const void* q, int64_t q_stri
     return FASTNN_ERR_INVALID;
   if (n == 0) return FASTNN_OK;
   FASTNN_TRY(row_checks(q, q_stride, static_cast<int64_t>(heads_q) * store->d));
-  if (!store->k_mean || !aligned(store->k_mean, 16) || !store->page_table || !store->lens ||
-      !store->cu || !out_pages || !aligned(out_pages, 4) || !aligned(workspace, kAlign))
+  if (!store->k_mean || !aligned(store->k_mean, 16) || !index_arrays(store) || !out_pages ||
+      !aligned(out_pages, 4) || !aligned(workspace, kAlign))
     return FASTNN_ERR_INVALID;
   const size_t need = fastnn_select_workspace_size(store, n, heads_q, max_new);
   if (!workspace && need > kAlign) return FASTNN_ERR_INVALID;

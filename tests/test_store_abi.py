@@ -255,3 +255,18 @@ def test_batches_beyond_what_the_kernels_count_are_refused(lib):
     assert lib.fastnn_attend_workspace_size(s, top, 2, top, 0) > 0
     assert lib.fastnn_attend_workspace_size(s, top, 4, top - 9, 0) > 0
     assert lib.fastnn_select_workspace_size(s, top, 2, top) > 0
+
+
+def test_index_arrays_must_be_aligned(lib):
+    """An address that is no multiple of its element's size would fault on the device."""
+    big = 1 << 40
+    for name in ("page_table", "lens", "cu"):
+        for off in (1, 2):
+            s = _desc(**{name: FAKE + off})
+            assert lib.fastnn_store_append(s, FAKE, 128, FAKE, 128, 5, 3, None, FAKE, 256, None) == -1, name
+            assert lib.fastnn_attend(s, FAKE, 256, 5, 4, 3, 1, 1.0, None, 0, FAKE, FAKE, FAKE, big, None) == -1, name
+            assert lib.fastnn_select_pages(s, FAKE, 256, 5, 4, 3, 1, 0, 1, 4, FAKE, FAKE, big, None) == -1, name
+    assert lib.fastnn_attend(_desc(), FAKE, 256, 5, 4, 3, 1, 1.0, FAKE + 2, 4, FAKE, FAKE, FAKE, big, None) == -1
+    for r in (_rot(pos=FAKE + 2), _rot(freq=FAKE + 4)):
+        assert lib.fastnn_rotary(FAKE, 128, 5, 2, 64, fnn.FASTNN_F16, r, 0, FAKE, 128, None) == -1
+        assert lib.fastnn_store_append(_desc(), FAKE, 128, FAKE, 128, 5, 3, r, FAKE, 256, None) == -1
