@@ -409,8 +409,9 @@ int fastnn_store_append(const fastnn_store *store, const void *k, int64_t k_stri
  *   [n][heads_q] float32, the natural logarithm of the sum of the
  *   exponentials. A token that sees nothing gets out = 0, lse = -infinity.
  *   Products and sums in fp32; the weights of the second product are rounded
- *   to dtype (relative 2^-9 for bf16, far below the rounding of a result that
- *   averages them); out is rounded once.
+ *   to dtype (half a step: relative 2^-8 for bf16, 2^-11 for half), and out is
+ *   rounded once. For values of mixed sign the two roundings are of one size:
+ *   the error of out is then about sqrt(2) times that of one rounding.
  *   Keys and values at positions that some token of the call sees must be
  *   finite; what lies behind lens in a page is never used. NaN in a row of q
  *   makes that row of out and lse NaN (where it sees anything), and no other.

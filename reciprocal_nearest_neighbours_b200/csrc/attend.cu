@@ -383,8 +383,8 @@ attend_rows_kernel(AttendArgs a) {
           sum[n][1] = y[n][1] + y[n][3];
         }
       }
-      // The weights go to the tensor cores in the store's 16-bit type, turned
-      // from (position, row) to the (row, position) fragments of an operand.
+      // The weights go to the tensor cores rounded to the store's 16-bit type (the
+      // operands of a product have one type), turned from (position, row) to the (row, position) fragments of an operand.
       uint32_t p[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -651,7 +651,8 @@ int rows_width(const AttendArgs& a, cudaStream_t st) {
 }  // namespace
 
 // How many blocks share the positions of a row tile. The lengths are on the
-// device; the table's width bounds them. About four waves of blocks (two a SM)
+// device; the table's width bounds them (and is taken for them: under a table far
+// wider than its longest sequence fewer blocks have work). About four waves of blocks (two a SM)
 // even out ragged lengths, a split is at least 256 positions long, and splits
 // beyond a row's length cost an empty block each.
 void attend_plan(AttendArgs& a) {

@@ -34,9 +34,12 @@
 // Bound by: exponentials (16 a clock and SM: 1024 clocks a tile of 128 x 128) and,
 // at 128 elements a head, products (1024 clocks a tile too), whose phases overlap
 // between the two query tiles in part. Measured: 2048 tokens over 16384, 32 / 8
-// heads of 128, 425 us (1.2 PFLOP/s, tensor pipe 61% busy; 500 us under the
-// power cap of a long run); 12288 rows over 196608 keys of 24, values of 8, 700 to 765 us
-// (exponentials 69% busy); 8 x 576 tokens over up to 9792, 12 heads of 64, 172 us.
+// heads of 128, 431 us (1.2 PFLOP/s, tensor pipe 60% busy; 490 to 500 us under the
+// power cap of a long run); 12288 rows over 196608 keys of 24, values of 8, 708 us
+// (exponentials 70% busy); 8 x 576 tokens over up to 9792, 12 heads of 64, 174 us.
+// The weights are rounded to the store's 16-bit type: the operands of a
+// product have one type, and a second product for what the rounding loses would
+// take half as much tensor time again.
 // Every wait is bounded; on expiry the kernel records FASTNN_ERR_TIMEOUT,
 // drains what it issued, frees its tensor memory and returns.
 #include <cuda.h>
@@ -61,7 +64,7 @@ constexpr int kSoftRegs = 216;
 constexpr int kOtherRegs = 72;
 constexpr int kBlk = 128;          // rows of a tile (queries, keys)
 // An item's fixed cost (its queries, the first scores, the output), in key tiles.
-// 8 images of 576 tokens, with 1 / 2 / 4 / 6 / 8: 184 / 179 / 172 / 173 / 176 us.
+// 8 images of 576 tokens, with 1 / 2 / 4 / 6: 181 / 177 / 174 / 176 us.
 constexpr int kItemCost = 4;
 constexpr int kLeastShare = 2;     // a CTA's share is at least this many tiles and that cost
 constexpr float kMostSum = 256.f;
@@ -76,9 +79,11 @@ struct Tc {
   static constexpr int kCtl = kRing + kStages * kTile;
   static constexpr int kBlock = kBlk * 128;        // bytes of a 64-element column block
   // Of every 16 pairs of weights, so many by polynomial (14 instructions a pair
-  // against 16 clocks of the special-function unit). Measured with 2 / 5 / 7:
-  // 12288 queries over 196608 keys of 24 765 / 800 / 822 us; with 0 / 2 / 5: 2048
-  // over 16384, 32 heads of 128, 434 / 425 / 432 us.
+  // against 16 clocks of the special-function unit). Measured with 0 / 1 / 2 /
+  // 3 / 5: 12288 queries over 196608 keys of 24 731 / 731 / 706 / 712 / 749 us; 2048
+  // over 16384, 32 heads of 128, 436 / 433 / 431 / 436 / 441 us. (Its upper bound
+  // costs 10 to 15 us of the former; the largest argument by a maximum of three
+  // instead took 4 more.)
   static constexpr int kPolyPairs = 2;
   // Tensor memory columns of query tile w: scores at 128 w, O at kO + DP w, the
   // weights (packed in pairs, 64 columns) at kP + kPStep w: over the scores where

@@ -439,7 +439,8 @@ cudaError_t pick(const SelectArgs& a, cudaStream_t st) {
 bool is_step(int max_new) { return max_new < kStepTokens; }
 // A single token over few pages needs no scratch and one launch. (16 sequences of
 // 400 pages, 4 key heads: 1 token 19.5 us by one block, 19.8 by two kernels; 7 tokens
-// 80 and 38. Chunk kernels instead of the step's: 50 and 54.)
+// 80 and 38. Chunk kernels instead of the step's: 50 and 54. The table's width stands
+// for the number of pages: measured with tables no wider than the need.)
 bool is_whole(const StoreArgs& st, int max_new) { return max_new == 1 && st.width <= kWholeWidth; }
 
 template <typename T>

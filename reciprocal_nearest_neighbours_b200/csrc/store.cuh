@@ -189,6 +189,7 @@ int launch_attend_rows(const AttendArgs& a, int dtype, cudaStream_t st);
 // floats of a.part that it needs. Rows 32 / 64 / 128, 16 sequences of 4096 positions, 8
 // key heads of 128: 76 / 79 / 83 us, the few-rows kernel 77 / 126 / 186; one of 8192: 34 /
 // 34 / 36 and 28 / 32 / 43; 8 of 4096, 12 heads of 64: 55 / 56 / 59 and 42 / 63 / 105.
+// (Sequences of one batch had equally many rows; a long one takes the others along.)
 constexpr int kTcRows = 64;
 bool attend_tc_takes(const AttendArgs& a);
 size_t attend_tc_floats(const AttendArgs& a);
